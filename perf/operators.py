@@ -339,7 +339,9 @@ def _run_own(st):
     case = st["case"]
     op = case["op"]
     if op == "plan":
-        p = gmla.plan_batch(st["cached"], st["new"], st["table"], st["free"], st["page"], st["tokens"])
+        # a serving loop keeps the plan's buffers from step to step
+        p = st["plan"] = gmla.plan_batch(st["cached"], st["new"], st["table"], st["free"], st["page"], st["tokens"],
+                                         out=st.get("plan"))
         return dict(block_table=st["table"], seq_lens=p.seq_lens, cu_seqlens=p.cu_seqlens, positions=p.positions,
                     seq_ids=p.seq_ids, slots=p.slots, pages_used=p.pages_used)
     if op == "norm":
