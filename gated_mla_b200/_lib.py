@@ -23,6 +23,7 @@ GMLA_BF16 = 0
 GMLA_FP32 = 1
 GMLA_CACHE_SAME = 0
 GMLA_CACHE_FP8_E4M3 = 1
+GMLA_CACHE_FP8_BLOCK = 2
 GMLA_GATE_CHANNEL = 0
 GMLA_GATE_HEAD = 1
 GMLA_GATE_HEAD_TOPK = 2
@@ -64,7 +65,13 @@ class gmla_cache(ctypes.Structure):
         ("num_pages", ctypes.c_int32),
         ("max_pages_per_seq", ctypes.c_int32),
         ("block_table", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("scale_block", ctypes.c_int32),
     ]
+
+
+class gmla_w4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("group", ctypes.c_int32)]
 
 
 class GmlaError(RuntimeError):
@@ -85,6 +92,8 @@ def _load() -> ctypes.CDLL:
     cfgp = ctypes.POINTER(gmla_config)
     wp = ctypes.POINTER(gmla_weights)
     cp = ctypes.POINTER(gmla_cache)
+    w4p = ctypes.POINTER(gmla_w4)
+    N = ctypes.c_int64
     sig = {
         "gmla_latent_project": (st, [cfgp, wp, P, I, P, P, cp, P, P, P, S, P]),
         "gmla_decode": (st, [cfgp, wp, P, P, cp, P, I, P, P, S, P]),
@@ -94,6 +103,11 @@ def _load() -> ctypes.CDLL:
         "gmla_decode_merge_workspace_size": (S, [cfgp, I]),
         "gmla_prefill": (st, [cfgp, wp, P, P, cp, P, I, I, I, P, P, S, P]),
         "gmla_gate_out": (st, [cfgp, wp, P, I, P, P, P, S, P]),
+        "gmla_gate_out_w4": (st, [cfgp, w4p, P, I, P, P, P, S, P]),
+        "gmla_gate_out_w4_workspace_size": (S, [cfgp, I]),
+        "gmla_plan_batch": (st, [P, P, I, P, I, I, P, I, I, P, P, P, P, P, P, P, S, P]),
+        "gmla_add_rms_norm": (st, [I, P, N, P, N, P, ctypes.c_float, I, I, P, N, P, N, P, P, I, P]),
+        "gmla_cache_append": (st, [cfgp, cp, P, N, P, P, I, I, P, S, P]),
         "gmla_latent_project_workspace_size": (S, [cfgp, I]),
         "gmla_decode_workspace_size": (S, [cfgp, I]),
         "gmla_prefill_workspace_size": (S, [cfgp, I, I]),
@@ -162,6 +176,32 @@ def gmla_prefill(cfg, w, q, gate_logits, cache, cu_seqlens, B, T, max_seqlen, o,
 
 def gmla_gate_out(cfg, w, o, T, gate_logits, y, ws, ws_bytes, stream):
     return lib.gmla_gate_out(ctypes.byref(cfg), ctypes.byref(w), o, T, gate_logits, y, ws, ws_bytes, stream)
+
+
+def gmla_gate_out_w4(cfg, w4, o, T, gate_logits, y, ws, ws_bytes, stream):
+    return lib.gmla_gate_out_w4(ctypes.byref(cfg), ctypes.byref(w4), o, T, gate_logits, y, ws, ws_bytes, stream)
+
+
+def gmla_gate_out_w4_workspace_size(cfg, T):
+    return lib.gmla_gate_out_w4_workspace_size(ctypes.byref(cfg), T)
+
+
+def gmla_plan_batch(cached_lens, new_lens, B, free_pages, n_free, page_size, block_table, max_pages_per_seq, T,
+                    seq_lens, cu_seqlens, positions, seq_ids, slots, pages_used, ws, ws_bytes, stream):
+    return lib.gmla_plan_batch(cached_lens, new_lens, B, free_pages, n_free, page_size, block_table,
+                               max_pages_per_seq, T, seq_lens, cu_seqlens, positions, seq_ids, slots, pages_used, ws,
+                               ws_bytes, stream)
+
+
+def gmla_add_rms_norm(dtype, x, x_stride, residual, residual_stride, weight, eps, T, d, residual_out,
+                      residual_out_stride, out, out_stride, codes, scales, group, stream):
+    return lib.gmla_add_rms_norm(dtype, x, x_stride, residual, residual_stride, weight, eps, T, d, residual_out,
+                                 residual_out_stride, out, out_stride, codes, scales, group, stream)
+
+
+def gmla_cache_append(cfg, cache, latents, latent_stride, cu_seqlens, seq_lens, B, T, ws, ws_bytes, stream):
+    return lib.gmla_cache_append(ctypes.byref(cfg), ctypes.byref(cache), latents, latent_stride, cu_seqlens, seq_lens,
+                                 B, T, ws, ws_bytes, stream)
 
 
 def gmla_decode_workspace_size(cfg, B):

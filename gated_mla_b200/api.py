@@ -1,14 +1,16 @@
 """Torch-facing marshalling over the C ABI (device memory and streams only).
 
 ``GatedMLA`` holds a configuration and device weight tensors and exposes the
-four library calls. Outputs and workspaces are torch allocations; every
+library's calls on a layer. ``plan_batch`` (block table, positions and slots of a
+step) and ``add_rms_norm`` stand beside it, and ``W4Weight`` / ``quantize_w4`` hold a
+weight in 4 bits. Outputs and workspaces are torch allocations; every
 computation happens inside libgmla.so on the current CUDA stream.
 """
 from __future__ import annotations
 
 import dataclasses
 import math
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -35,6 +37,10 @@ class LatentCache:
     data: torch.Tensor
     block_table: Optional[torch.Tensor] = None   # int32 [B, max_pages_per_seq] for paged
     batch: int = 0
+    # block-scaled FP8 cache: fp32, one scale for each block of scale_block rows
+    # ([pages, page // block] for paged, [B, ceil(cap / block)] for contiguous)
+    scales: Optional[torch.Tensor] = None
+    scale_block: int = 0          # 0 with a paged cache: page // scales.shape[1]
 
     @property
     def paged(self) -> bool:
@@ -54,15 +60,200 @@ class LatentCache:
         else:
             c.batch = self.data.shape[0]
             c.capacity = self.data.shape[1]
+        if self.scales is not None:
+            n, block = self.scales.shape[1], self.scale_block
+            rows = self.data.shape[1]
+            if not block:
+                if not self.paged:
+                    raise ValueError("a contiguous block-scaled cache needs scale_block")
+                block = rows // max(n, 1)
+            if (self.scales.dtype != torch.float32 or self.scales.device != self.data.device
+                    or self.scales.shape[0] != self.data.shape[0] or block < 1 or n != -(-rows // block)):
+                raise ValueError("scales must be float32 [pages, page // block] (paged) or [B, ceil(capacity / block)] "
+                                 "on the cache's device")
+            c.scales = _p(self.scales)
+            c.scale_block = block
         return c
+
+
+def _check(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> None:
+    """A tensor argument of the calls below: its type, its sizes (None: any) and its device."""
+    if t.dtype != dtype or t.device != device or t.dim() != len(shape) or any(
+            n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _stream_of(t: torch.Tensor) -> int:
+    """The current stream, which has to be one of the tensor's device."""
+    if not t.is_cuda:
+        raise ValueError("gated_mla_b200 takes CUDA tensors only")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}: "
+                         "call inside torch.cuda.device(...)")
+    return torch.cuda.current_stream().cuda_stream
+
+
+class _Scratch:
+    """Workspaces by (call, stream): calls on different streams never share one, and a
+    call under graph capture gets one of its own, which belongs to that graph."""
+
+    def __init__(self):
+        self._held = {}
+
+    def get(self, key: str, nbytes: int, device: torch.device, stream: int) -> torch.Tensor:
+        capturing = torch.cuda.is_current_stream_capturing()
+        ws = None if capturing else self._held.get((key, device.index, stream))
+        if ws is None or ws.numel() < nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            if not capturing:
+                self._held[(key, device.index, stream)] = ws
+            L.check(L.gmla_clear_status(ws.data_ptr(), stream), "clear_status")
+        return ws
+
+    def sync_status(self) -> None:
+        for (key, index, stream), ws in self._held.items():
+            with torch.cuda.device(index):
+                L.check(L.gmla_sync_status(ws.data_ptr(), stream), f"device status ({key})")
+
+
+_scratch = _Scratch()
+
+
+def sync_status() -> None:
+    """Synchronise and raise if a plan_batch call reported a batch that cannot be."""
+    _scratch.sync_status()
+
+
+class BatchPlan(NamedTuple):
+    """What one step of a batch over a paged cache needs (see plan_batch)."""
+    seq_lens: torch.Tensor      # int32 [B]: rows of each sequence, the new ones included
+    cu_seqlens: torch.Tensor    # int32 [B + 1]: packed token offsets
+    positions: torch.Tensor     # int32 [n_tokens], -1 behind the last sequence
+    seq_ids: torch.Tensor       # int32 [n_tokens]
+    slots: torch.Tensor         # int64 [n_tokens]: page * page_size + row
+    pages_used: torch.Tensor    # int32 [1]: how many of the free pages were taken
+
+
+def plan_batch(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+               page_size: int, n_tokens: int, out: Optional[BatchPlan] = None) -> BatchPlan:
+    """The plan of one step, made on the GPU from its request lengths.
+
+    ``cached_lens`` and ``new_lens`` are int32 [B]; ``block_table`` (int32 [B, max_pages])
+    gets the entries of the pages that new rows begin, taken from ``free_pages`` in the
+    order of the sequences. ``n_tokens`` is the number of token rows, at least the sum of
+    new_lens; rows behind the last sequence get -1. ``out`` reuses the buffers of an
+    earlier plan of the same sizes. A batch that does not fit is planned as empty and
+    reported by ``sync_status``.
+    """
+    dev, B, T = cached_lens.device, cached_lens.shape[0], int(n_tokens)
+    stream = _stream_of(cached_lens)
+    i32 = torch.int32
+    _check(cached_lens, "cached_lens", i32, (B,), dev)
+    _check(new_lens, "new_lens", i32, (B,), dev)
+    _check(block_table, "block_table", i32, (B, None), dev)
+    _check(free_pages, "free_pages", i32, (None,), dev)
+    if T < 0:
+        raise ValueError("n_tokens must be >= 0")
+    if out is None:
+        new = lambda n, t=i32: torch.empty(n, dtype=t, device=dev)  # noqa: E731
+        out = BatchPlan(new(B), new(B + 1), new(T), new(T), new(T, torch.int64), new(1))
+    else:
+        for name, n, t in (("seq_lens", B, i32), ("cu_seqlens", B + 1, i32), ("positions", T, i32), ("seq_ids", T, i32),
+                           ("slots", T, torch.int64), ("pages_used", 1, i32)):
+            _check(getattr(out, name), "out." + name, t, (n,), dev)
+    ws = _scratch.get("plan_batch", 256, dev, stream)
+    L.check(L.gmla_plan_batch(_p(cached_lens), _p(new_lens), B, _p(free_pages), free_pages.shape[0], int(page_size),
+                              _p(block_table), block_table.shape[1], T, _p(out.seq_lens), _p(out.cu_seqlens),
+                              _p(out.positions), _p(out.seq_ids), _p(out.slots), _p(out.pages_used), ws.data_ptr(),
+                              ws.numel(), stream), "gmla_plan_batch")
+    return out
+
+
+class NormOut(NamedTuple):
+    """Outputs of add_rms_norm; those not asked for are None."""
+    out: Optional[torch.Tensor]        # [T, d]: the normalised rows
+    residual: Optional[torch.Tensor]   # [T, d]: x + residual
+    codes: Optional[torch.Tensor]      # float8_e4m3fn [T, d]
+    scales: Optional[torch.Tensor]     # float32 [T, ceil(d / group)]
+
+
+def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None, *,
+                 eps: float = 1e-6, fp8_group: int = 0, out: Optional[torch.Tensor] = None,
+                 residual_out: Optional[torch.Tensor] = None, want_out: bool = True) -> NormOut:
+    """s = x + residual, y = s / sqrt(mean(s^2) + eps) * weight, over the rows of x [T, d].
+
+    Rows may be strided (their elements contiguous). With ``fp8_group`` (32, 64, 128 or
+    256) y also comes as E4M3 codes with one scale for each group of columns;
+    ``want_out=False`` then leaves the unquantised y out. ``residual_out`` may be
+    ``residual`` itself, ``out`` may be ``x``.
+    """
+    stream = _stream_of(x)
+    if x.dtype not in _DT or x.dim() != 2:
+        raise ValueError("x must be bfloat16 or float32 [T, d]")
+    dev, (T, d) = x.device, x.shape
+    if out is None and want_out:
+        out = torch.empty(T, d, dtype=x.dtype, device=dev)
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out goes with a residual")
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(T, d, dtype=x.dtype, device=dev)
+    codes = scales = None
+    if fp8_group:
+        if fp8_group < 0:
+            raise ValueError("fp8_group must be 0, 32, 64, 128 or 256")
+        codes = torch.empty(T, d, dtype=torch.float8_e4m3fn, device=dev)
+        scales = torch.empty(T, -(-d // fp8_group), dtype=torch.float32, device=dev)
+    rows = []
+    for name, t in (("x", x), ("residual", residual), ("residual_out", residual_out), ("out", out)):
+        if t is None:
+            rows += [None, 0]
+            continue
+        _check(t, name, x.dtype, (T, d), dev)
+        if d > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        rows += [t.data_ptr(), t.stride(0) if T > 1 else d]
+    if weight is not None:
+        _check(weight, "weight", x.dtype, (d,), dev)
+    L.check(L.gmla_add_rms_norm(_DT[x.dtype], *rows[:4], _p(weight), eps, T, d, *rows[4:], _p(codes), _p(scales),
+                                fp8_group, stream), "gmla_add_rms_norm")
+    return NormOut(out, residual_out, codes, scales)
+
+
+@dataclasses.dataclass
+class W4Weight:
+    """A weight matrix [N, K] in 4 bits: W[n, k] = (code - 8) * scales[n, k // group]."""
+    codes: torch.Tensor       # uint8 [N, K // 2], even k in the low nibble
+    scales: torch.Tensor      # bfloat16 [N, K // group]
+    group: int = 128
+
+    def struct(self) -> L.gmla_w4:
+        w = L.gmla_w4()
+        w.codes, w.scales, w.group = _p(self.codes), _p(self.scales), self.group
+        return w
+
+
+def quantize_w4(weight: torch.Tensor, group: int = 128) -> W4Weight:
+    """Nearest 4-bit codes of a weight [N, K], the scale of a group its largest magnitude / 7 (done once, at load time)."""
+    N, K = weight.shape
+    if group not in (32, 64, 128) or K % group:
+        raise ValueError("group must be 32, 64 or 128 and divide K")
+    w = weight.float().view(N, K // group, group)
+    scales = (w.abs().amax(-1) / 7).to(torch.bfloat16)
+    step = scales.float().unsqueeze(-1)
+    code = torch.where(step > 0, torch.round(w / step), torch.zeros((), device=w.device)).clamp(-8, 7) + 8
+    code = code.to(torch.uint8).view(N, K)
+    return W4Weight((code[:, 0::2] | (code[:, 1::2] << 4)).contiguous(), scales.contiguous(), group)
 
 
 class GatedMLA:
     def __init__(self, *, d_model: int, n_heads: int, d_h: int, d_c: int, d_rope: int = 0,
                  gate_mode: str = "channel", softmax_scale: Optional[float] = None,
                  rope_base: float = 10000.0, dtype: torch.dtype = torch.bfloat16,
-                 weights: dict, d_cq: int = 0, gate_topk: int = 0, cache_fp8: bool = False,
+                 weights: dict, d_cq: int = 0, gate_topk: int = 0, cache_fp8=False,
                  cache_scale: float = 1.0):
+        # cache_fp8: False, True (E4M3 codes, one scale for the cache) or "block" (one scale for each block of rows)
+        if cache_fp8 not in (False, True, "block"):
+            raise ValueError("cache_fp8 must be False, True or 'block'")
         self.dtype = dtype
         self.cfg = L.gmla_config()
         self.cfg.d_model, self.cfg.n_heads, self.cfg.d_h, self.cfg.d_c, self.cfg.d_rope = (
@@ -74,13 +265,16 @@ class GatedMLA:
         self.cfg.rope_base = rope_base
         self.cfg.dtype = _DT[dtype]
         self.cfg.d_cq = d_cq
-        self.cfg.cache_dtype = L.GMLA_CACHE_FP8_E4M3 if cache_fp8 else L.GMLA_CACHE_SAME
+        self.cfg.cache_dtype = (L.GMLA_CACHE_FP8_BLOCK if cache_fp8 == "block"
+                                else L.GMLA_CACHE_FP8_E4M3 if cache_fp8 else L.GMLA_CACHE_SAME)
         self.cfg.cache_scale = cache_scale
         self.weights = dict(weights)
         self.w = L.gmla_weights()
         for k in ("W_c", "W_kr", "W_q", "W_qr", "W_k", "W_v", "W_g", "b_g", "W_o", "W_dq", "W_uq"):
             setattr(self.w, k, _p(self.weights.get(k)))
         self._ws = {}
+        self._scratch = _Scratch()
+        self._staging_cfg = None
 
     # -- sizes
     @property
@@ -104,9 +298,19 @@ class GatedMLA:
         return torch.cuda.current_stream().cuda_stream
 
     # -- the four calls
-    def latent_project(self, x, positions, seq_ids, cache: LatentCache, q_out=None, gate_logits=None):
+    @property
+    def block_scaled(self) -> bool:
+        return self.cfg.cache_dtype == L.GMLA_CACHE_FP8_BLOCK
+
+    def latent_project(self, x, positions, seq_ids, cache: LatentCache, q_out=None, gate_logits=None, *,
+                       cu_seqlens=None, seq_lens=None):
+        """Project the tokens and write their latents into the cache. A block-scaled cache
+        takes the packing of the tokens too (``cu_seqlens`` and ``seq_lens``, as cache_append):
+        the latents go through a bf16 buffer of the step's rows."""
         T = x.shape[0]
         c = self.cfg
+        if self.block_scaled:
+            return self._project_and_append(x, cache, q_out, gate_logits, cu_seqlens, seq_lens)
         if q_out is None:
             q_out = torch.empty(T, c.n_heads, c.d_h + c.d_rope, dtype=self.dtype, device=x.device)
         if gate_logits is None:
@@ -124,6 +328,8 @@ class GatedMLA:
         if o_out is None:
             o_out = torch.empty(B, c.n_heads * c.d_h, dtype=self.dtype, device=q.device)
         nb = L.gmla_decode_workspace_size(c, B)
+        if ws is None and self.block_scaled:
+            ws = self._scratch.get("decode", nb, q.device, _stream_of(q))
         if ws is None:
             ws = self.workspace("decode", nb, q.device)
         L.check(L.gmla_decode(c, self.w, _p(q), _p(gate_logits), cache.struct(), _p(seq_lens), B,
@@ -154,17 +360,96 @@ class GatedMLA:
                                 self._stream()), "gmla_gate_out")
         return y_out
 
+    def cache_append(self, latents, cu_seqlens, seq_lens, cache: LatentCache) -> None:
+        """Append the new latent rows [T, d_c] (packed by sequence, rows may be strided) to a
+        block-scaled cache: sequence b's rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 go to its
+        last positions, seq_lens[b] (the new rows included) being its length afterwards."""
+        stream = _stream_of(latents)
+        dev, c = latents.device, self.cfg
+        B = seq_lens.shape[0]
+        _check(latents, "latents", self.dtype, (None, c.d_c), dev)
+        _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
+        _check(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+        T = latents.shape[0]
+        if latents.stride(1) != 1:
+            raise ValueError("latents: the elements of a row must be contiguous")
+        ws = self._scratch.get("append", 256, dev, stream)
+        L.check(L.gmla_cache_append(c, self._cache_struct(cache, dev), latents.data_ptr(),
+                                    latents.stride(0) if T > 1 else c.d_c, _p(cu_seqlens), _p(seq_lens), B, T,
+                                    ws.data_ptr(), ws.numel(), stream), "gmla_cache_append")
+
+    def _cache_struct(self, cache: LatentCache, device) -> L.gmla_cache:
+        """The cache argument of a block-scaled layer."""
+        if cache.scales is None:
+            raise ValueError("a block-scaled layer needs a cache with scales")
+        if cache.data.device != device or cache.data.element_size() != 1 or cache.data.shape[-1] != self.row:
+            raise ValueError(f"a block-scaled cache holds 1-byte codes in rows of {self.row} on {device}")
+        return cache.struct()
+
+    def _project_and_append(self, x, cache, q_out, gate_logits, cu_seqlens, seq_lens):
+        if cu_seqlens is None or seq_lens is None:
+            raise ValueError("a block-scaled cache needs cu_seqlens and seq_lens")
+        stream = _stream_of(x)
+        T, dev = x.shape[0], x.device
+        if self._staging_cfg is None:      # the same layer over a bf16 cache: one sequence, row t the latent of token t
+            cfg = L.gmla_config.from_buffer_copy(self.cfg)
+            cfg.cache_dtype = L.GMLA_CACHE_SAME
+            self._staging_cfg = cfg
+        cfg = self._staging_cfg
+        if cfg.d_rope:
+            raise ValueError("a block-scaled cache covers NoPE")
+        if q_out is None:
+            q_out = torch.empty(T, cfg.n_heads, cfg.d_h, dtype=self.dtype, device=dev)
+        if gate_logits is None:
+            gate_logits = torch.empty(T, self.G, dtype=torch.float32, device=dev)
+        rows = torch.empty(max(T, 1), cfg.d_c, dtype=self.dtype, device=dev)
+        staging = LatentCache(rows.view(1, max(T, 1), cfg.d_c))
+        order = torch.arange(T, dtype=torch.int32, device=dev)
+        slot = torch.zeros(T, dtype=torch.int32, device=dev)
+        ws = self._scratch.get("project", L.gmla_latent_project_workspace_size(cfg, T), dev, stream)
+        L.check(L.gmla_latent_project(cfg, self.w, _p(x), T, _p(order), _p(slot), staging.struct(), _p(q_out),
+                                      _p(gate_logits), ws.data_ptr(), ws.numel(), stream), "gmla_latent_project")
+        self.cache_append(rows[:T], cu_seqlens, seq_lens, cache)
+        return q_out, gate_logits
+
+    def gate_out_w4(self, o, w4: W4Weight, gate_logits=None, y_out=None):
+        """gate_out with W_o in 4 bits (``w4`` is [d_model, H*d_h])."""
+        stream = _stream_of(o)
+        c, dev, T = self.cfg, o.device, o.shape[0]
+        K = c.n_heads * c.d_h
+        _check(o, "o", self.dtype, (T, K), dev)
+        if w4.group not in (32, 64, 128) or K % w4.group:
+            raise ValueError("w4.group must be 32, 64 or 128 and divide H*d_h")
+        _check(w4.codes, "w4.codes", torch.uint8, (c.d_model, K // 2), dev)
+        _check(w4.scales, "w4.scales", torch.bfloat16, (c.d_model, K // w4.group), dev)
+        if gate_logits is not None:
+            _check(gate_logits, "gate_logits", torch.float32, (T, self.G), dev)
+        if y_out is None:
+            y_out = torch.empty(T, c.d_model, dtype=self.dtype, device=dev)
+        else:
+            _check(y_out, "y_out", self.dtype, (T, c.d_model), dev)
+        ws = self._scratch.get("gate_out_w4", L.gmla_gate_out_w4_workspace_size(c, T), dev, stream)
+        L.check(L.gmla_gate_out_w4(c, w4.struct(), _p(o), T, _p(gate_logits), _p(y_out), ws.data_ptr(), ws.numel(),
+                                   stream), "gmla_gate_out_w4")
+        return y_out
+
     def sync_status(self):
         """Synchronise and raise if any kernel reported a device-side fault."""
+        self._scratch.sync_status()
         for key, ws in self._ws.items():
             L.check(L.gmla_sync_status(ws.data_ptr(), self._stream()), f"device status ({key})")
 
     # -- whole steps
-    def decode_step(self, x, cache: LatentCache, seq_lens, positions, seq_ids):
-        """One decode step: project (writing each new latent row), attend, gate, W_o."""
-        q, g = self.latent_project(x, positions, seq_ids, cache)
+    def decode_step(self, x, cache: LatentCache, seq_lens, positions, seq_ids, *, cu_seqlens=None,
+                    w4: Optional[W4Weight] = None):
+        """One decode step: project (writing each new latent row), attend, gate, W_o (in 4
+        bits when ``w4`` is given). A block-scaled cache needs the step's ``cu_seqlens``."""
+        if self.block_scaled:
+            q, g = self.latent_project(x, positions, seq_ids, cache, cu_seqlens=cu_seqlens, seq_lens=seq_lens)
+        else:
+            q, g = self.latent_project(x, positions, seq_ids, cache)
         o = self.decode(q, g, cache, seq_lens)
-        return self.gate_out(o)
+        return self.gate_out(o) if w4 is None else self.gate_out_w4(o, w4)
 
     def prefill_step(self, x, cache: LatentCache, cu_seqlens, max_seqlen, positions, seq_ids):
         q, g = self.latent_project(x, positions, seq_ids, cache)

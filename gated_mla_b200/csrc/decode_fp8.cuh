@@ -17,6 +17,15 @@
 // its A operand). Scores are (S[h] + S[HG + h]) * sigma * cache_scale; the
 // weighted sum is (O^T[h] + O^T[HG + h]) * cache_scale / kPScale.
 //
+// With one scale s_t for every block of token rows (BLK; c = s_t c~) the weighted
+// sum's weights are p_t s_t, whose spread adds to that of p_t. So the running
+// reference m follows u_t = z_t + log2 s_t, P' = kPScale 2^(u - m) carries the scale
+// into the product, and the softmax sum takes 2^(u - m) / s_t. P' gets a third
+// e4m3 term, and each term is stored 32 times finer than the one before
+// (P' = hi + lo / 32 + lo2 / 1024, in columns of their own): weights 2^-24 below the
+// largest still count, as they must when one token far outweighs a long
+// context's tail. At N = 3 HG <= 96 an MMA costs what it does at 2 HG.
+//
 // Kernels: decode_absorb_fp8 (q_lat, its scale and hi/lo codes; its last block
 // builds the split plan as decode_absorb_plan does), decode_attn_fp8 (below),
 // then decode_merge and the W_v GEMM of the bf16 path.
@@ -49,6 +58,23 @@ __device__ __forceinline__ void split_e4m3(float v, uint8_t& hi, uint8_t& lo) {
   hi = to_e4m3(v);
   lo = to_e4m3(v - from_e4m3(hi));
 }
+// Two values as e4m3 terms, `n` of them, each 32 times finer than the one before
+// (v = t0 + t1 / 32 + t2 / 1024): codes of the pair in the low two bytes of t[i].
+template <int n>
+__device__ __forceinline__ void terms_e4m3x2(float a, float b, uint32_t (&t)[n]) {
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    t[i] = c;
+    if (i + 1 < n) {
+      const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3));
+      a = (a - __low2float(h)) * 32.f;
+      b = (b - __high2float(h)) * 32.f;
+    }
+  }
+}
+// The scales of a block-scaled cache lie in [2^-32, 2^32]; one outside (or NaN) is a fault.
+constexpr float kScaleMin = 2.3283064365386963e-10f, kScaleMax = 4294967296.f;
 // byte offset of (row, col) in a K-major tile of 128-byte rows with the 128-byte swizzle
 __device__ __forceinline__ uint32_t sw128_byte(uint32_t row, uint32_t col) {
   return row * 128u + ((((col >> 4) ^ row) & 7u) << 4) + (col & 15u);
@@ -176,14 +202,16 @@ struct Dec8Smem {
 // the 256 columns of tensor memory it needs), so one CTA's loads, softmax and
 // MMAs overlap the other's; each CTA on its own is bound by the latency of
 // that chain, not by bandwidth. 32 heads: one CTA per SM with a deeper ring.
-template <int HG>
+template <int HG, bool BLK>
 struct Dec8Cfg {
-  static constexpr int kN2 = 2 * HG;                         // hi and lo columns
+  static constexpr int kN2 = 2 * HG;                         // hi and lo columns of the scores
+  static constexpr int kTerms = BLK ? 3 : 2;                 // e4m3 terms of P'
+  static constexpr int kNP = kTerms * HG;                    // columns of P' and of O^T
   static constexpr int kSG = HG >= 32 ? 2 : 1;               // softmax warp groups (head slices)
   static constexpr int kThreads = 64 + 128 * kSG;
   static constexpr int kCtasPerSm = HG == 16 ? 2 : 1;
   static constexpr int kQBytes = kNB8 * kN2 * 128;           // 4 boxes of [2 HG rows x 128 B]
-  static constexpr int kPBytes = ((kN2 * 128) + 1023) & ~1023;   // [2 HG rows x 128 tokens]
+  static constexpr int kPBytes = ((kNP * 128) + 1023) & ~1023;   // [terms x HG rows x 128 tokens]
   static constexpr int kStruct = (static_cast<int>(sizeof(Dec8Smem)) + 127) & ~127;
   static constexpr int kFixed = kQBytes + kPBytes + kStruct + 1024 /*align*/;
   // shared memory of an SM (233472 B) less 1 KB reserved per CTA
@@ -191,19 +219,20 @@ struct Dec8Cfg {
   static constexpr int kRingMax = (kBudget - kFixed) / kBox8;
   static constexpr int kRing = kRingMax > 16 ? 16 : kRingMax;
   static constexpr int kSmem = kRing * kBox8 + kFixed;
-  static constexpr int kTmemCols = 6 * kN2 <= 256 ? 256 : 512;   // 2 S^T buffers + 4 O^T chunks
+  static constexpr int kTmemCols = 2 * kN2 + 4 * kNP <= 256 ? 256 : 512;   // 2 S^T buffers + 4 O^T chunks
   // the next tile's boxes are probed by the parity of their full barrier, which
   // is unambiguous while box c - kRing has been waited for: true up to c =
   // (first box of this tile) + 2 kNB8 - 1 when kRing >= kNB8
   static_assert(kRing >= kNB8 + 1, "the ring holds more than one tile");
+  static_assert(2 * kN2 + 4 * kNP <= kTmemCols, "scores and sums fit tensor memory");
   static_assert(kCtasPerSm * kTmemCols <= 512, "tensor memory of the CTAs sharing an SM");
 };
 
-template <int HG>
+template <int HG, bool BLK>
 __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 : 1))
     decode_attn_fp8_kernel(const __grid_constant__ DecodeArgs a) {
-  using C = Dec8Cfg<HG>;
-  constexpr int NR = C::kRing, N2 = C::kN2;
+  using C = Dec8Cfg<HG, BLK>;
+  constexpr int NR = C::kRing, N2 = C::kN2, NP = C::kNP;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;
@@ -244,7 +273,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
   const int seg_lo = a.cta_first_seg[g];
   const int seg_hi = (seg_lo < a.cta_first_seg[g + 1]) ? a.cta_first_seg[g + 1] : seg_lo;
   const uint32_t tmem = sm->tmem;
-  const uint32_t tO = tmem + 2 * N2;   // O^T chunk j (latent dims 128 j ..) at columns tO + j N2
+  const uint32_t tO = tmem + 2 * N2;   // O^T chunk j (latent dims 128 j ..) at columns tO + j NP
 
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
@@ -313,7 +342,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
     // ------------------------------ MMA issuer ------------------------------
     if (lane == 0) {
       constexpr uint32_t idS = idesc_e4m3_f32(128, N2, false, false);
-      constexpr uint32_t idO = idesc_e4m3_f32(128, N2, true, false);
+      constexpr uint32_t idO = idesc_e4m3_f32(128, NP, true, false);
       const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(qs), p_a = smem_u32(pbuf);
       const uint64_t dRing = sdesc_sw128(ring_a, 16, 1024), dQ = sdesc_sw128(q_a, 16, 1024);
       const uint64_t dRingMN = sdesc_sw128(ring_a, kBox8, 1024);   // a box read as [tokens (K) x 128 latent dims (M)]
@@ -363,7 +392,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
             const uint64_t da = dRingMN + slot * (kBox8 / 16);
 #pragma unroll
             for (int kk = 0; kk < kTok / 32; ++kk)
-              umma_f8(tO + j * N2, da + kk * (4096 / 16), dP + kk * 2, idO, (!first || kk > 0) ? 1u : 0u);
+              umma_f8(tO + j * NP, da + kk * (4096 / 16), dP + kk * 2, idO, (!first || kk > 0) ? 1u : 0u);
             umma_commit(&sm->empty[slot]);
           }
           nbox += kNB8;
@@ -386,7 +415,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const int ltid = threadIdx.x - 64;
     const float NEG_INF = -__int_as_float(0x7f800000);
-    const float o_mul = a.cache_scale / kPScale;
+    const float o_mul = (BLK ? 1.f : a.cache_scale) / kPScale;
     uint32_t nbox = 0, ntile = 0, nseg = 0;
     bool ok = true;
     for (int si = seg_lo; si < seg_hi; ++si) {
@@ -404,8 +433,49 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
         m[h] = NEG_INF;
         lsum[h] = 0.f;
       }
+      // block scales: this thread's row of a tile has scale sc; the next tile's scale and
+      // the page of the tile after it are fetched while a tile is worked on
+      float sc = 1.f, sc_next = 1.f;
+      int page_next = 0;
+      auto scale_page = [&](int t) {   // page of this thread's row in tile t (0 where there is none)
+        const int pos = t * kTok + row;
+        if (!a.cache.paged || t >= sg.z || pos >= L || pos < S0) return 0;
+        return a.cache.block_table[static_cast<int64_t>(b) * a.cache.max_pages_per_seq + pos / a.cache.page_size];
+      };
+      auto scale_of = [&](int t, int page) {
+        const int pos = t * kTok + row;
+        if (t >= sg.z || pos >= L || pos < S0) return 1.f;
+        int64_t i;
+        if (a.cache.paged) {
+          if (page < 0 || page >= a.cache.num_pages) {
+            report_status(a.status, kStatusRange);
+            return 1.f;
+          }
+          i = (static_cast<int64_t>(page) * a.cache.page_size + pos % a.cache.page_size) >> a.scale_shift;
+        } else {
+          const int per = (a.cache.capacity + (1 << a.scale_shift) - 1) >> a.scale_shift;
+          i = static_cast<int64_t>(b) * per + (pos >> a.scale_shift);
+        }
+        return a.scales[i];
+      };
+      if (BLK) {
+        sc_next = scale_of(sg.y, scale_page(sg.y));
+        page_next = scale_page(sg.y + 1);
+      }
       for (int t = sg.y; t < sg.z; ++t, ++ntile) {
         const bool first = (t == sg.y);
+        float lg = 0.f, isc = 1.f;
+        if (BLK) {
+          sc = sc_next;
+          sc_next = scale_of(t + 1, page_next);
+          page_next = scale_page(t + 2);
+          if (!(sc >= kScaleMin && sc <= kScaleMax)) {
+            report_status(a.status, kStatusRange);
+            sc = 1.f;
+          }
+          lg = __log2f(sc);
+          isc = 1.f / sc;
+        }
         ok = ok && mbar_wait(&sm->s_full, ntile & 1, abort_flag, a.status);
         tc_fence_after();
         const uint32_t tS = tmem + (ntile & 1) * N2 + lane_off + h0;
@@ -418,7 +488,9 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            x[j] = rv ? (__uint_as_float(vh[j]) + __uint_as_float(vl[j])) * mul[c + j] : NEG_INF;
+            x[j] = !rv ? NEG_INF
+                   : BLK ? fmaf((__uint_as_float(vh[j]) + __uint_as_float(vl[j])) * mul[c + j], sc, lg)
+                         : (__uint_as_float(vh[j]) + __uint_as_float(vl[j])) * mul[c + j];
         };
         bool need = first;
 #pragma unroll
@@ -468,9 +540,9 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
 #pragma unroll 1
               for (int mc = 0; mc < kNB8; ++mc) {
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
+                for (int part = 0; part < C::kTerms; ++part) {
                   uint32_t v[16];
-                  const uint32_t col = tO + lane_off + mc * N2 + part * HG + h0 + c;
+                  const uint32_t col = tO + lane_off + mc * NP + part * HG + h0 + c;
                   tmem_ld16(col, v);
                   tmem_ld_wait();
 #pragma unroll
@@ -488,6 +560,24 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
         for (int c = 0; c < HT; c += 16) {
           float x[16];
           load16(c, x);
+          if constexpr (BLK) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const int h = h0 + c + j;
+              const float p0 = rv ? ex2_approx(x[j] - m[c + j]) : 0.f;
+              const float p1 = rv ? ex2_approx(x[j + 1] - m[c + j + 1]) : 0.f;
+              lsum[c + j] = fmaf(p0, isc, lsum[c + j]);
+              lsum[c + j + 1] = fmaf(p1, isc, lsum[c + j + 1]);
+              uint32_t term[C::kTerms];
+              terms_e4m3x2<C::kTerms>(p0 * kPScale, p1 * kPScale, term);
+#pragma unroll
+              for (int k = 0; k < C::kTerms; ++k) {
+                pbuf[sw128_byte(k * HG + h, row)] = static_cast<uint8_t>(term[k]);
+                pbuf[sw128_byte(k * HG + h + 1, row)] = static_cast<uint8_t>(term[k] >> 8);
+              }
+            }
+            continue;
+          }
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const int h = h0 + c + j;
@@ -541,15 +631,16 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
       for (int mc = 0; mc < kNB8; ++mc) {
 #pragma unroll
         for (int c = 0; c < HT; c += 16) {
-          uint32_t vh[16], vl[16];
-          tmem_ld16(tO + lane_off + mc * N2 + h0 + c, vh);
-          tmem_ld16(tO + lane_off + mc * N2 + HG + h0 + c, vl);
+          uint32_t vh[16], vl[16], vt[16];
+          tmem_ld16(tO + lane_off + mc * NP + h0 + c, vh);
+          tmem_ld16(tO + lane_off + mc * NP + HG + h0 + c, vl);
+          if (BLK) tmem_ld16(tO + lane_off + mc * NP + 2 * HG + h0 + c, vt);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            if (ok && h0 + c + j < hv)
-              a.o_part[(pbase + h0 + c + j) * kDc8 + mc * 128 + row] =
-                  (__uint_as_float(vh[j]) + __uint_as_float(vl[j])) * o_mul;
+            const float hi = __uint_as_float(vh[j]), lo = __uint_as_float(vl[j]);
+            const float v = BLK ? fmaf(fmaf(__uint_as_float(vt[j]), 1.f / 32.f, lo), 1.f / 32.f, hi) : hi + lo;
+            if (ok && h0 + c + j < hv) a.o_part[(pbase + h0 + c + j) * kDc8 + mc * 128 + row] = v * o_mul;
           }
         }
       }
@@ -569,10 +660,10 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
   }
 }
 
-template <int HG>
+template <int HG, bool BLK>
 static cudaError_t launch_attn_fp8(const DecodeArgs& a, cudaStream_t st) {
-  using C = Dec8Cfg<HG>;
-  auto k = decode_attn_fp8_kernel<HG>;
+  using C = Dec8Cfg<HG, BLK>;
+  auto k = decode_attn_fp8_kernel<HG, BLK>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   prof_begin(st, "decode_attn");

@@ -989,8 +989,8 @@ static cudaError_t launch_decode_fp8(DecodeArgs& a, cudaStream_t st) {
   prof_end(st);
   if (e != cudaSuccess) return e;
   switch (a.HG) {
-    case 16: e = launch_attn_fp8<16>(a, st); break;
-    case 32: e = launch_attn_fp8<32>(a, st); break;
+    case 16: e = a.scales ? launch_attn_fp8<16, true>(a, st) : launch_attn_fp8<16, false>(a, st); break;
+    case 32: e = a.scales ? launch_attn_fp8<32, true>(a, st) : launch_attn_fp8<32, false>(a, st); break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;

@@ -92,8 +92,10 @@ gmla_status check_cfg(const gmla_config* c) {
     return fail(GMLA_ERR_INVALID_ARG, "gate_mode must be one of the gmla_gate_mode values");
   if (c->gate_mode == GMLA_GATE_HEAD_TOPK && (c->gate_topk < 1 || c->gate_topk > c->n_heads))
     return fail(GMLA_ERR_INVALID_ARG, "gate_topk must be in [1, n_heads] for GMLA_GATE_HEAD_TOPK");
-  if (c->cache_dtype != GMLA_CACHE_SAME && c->cache_dtype != GMLA_CACHE_FP8_E4M3)
+  if (c->cache_dtype < GMLA_CACHE_SAME || c->cache_dtype > GMLA_CACHE_FP8_BLOCK)
     return fail(GMLA_ERR_INVALID_ARG, "cache_dtype must be a gmla_cache_dtype value");
+  if (c->cache_dtype == GMLA_CACHE_FP8_BLOCK && c->dtype != GMLA_BF16)
+    return fail(GMLA_ERR_INVALID_ARG, "an FP8 cache needs the bf16 dtype");
   if (c->cache_dtype == GMLA_CACHE_FP8_E4M3 &&
       (c->dtype != GMLA_BF16 || !(c->cache_scale > 0.f) || !std::isfinite(c->cache_scale)))
     return fail(GMLA_ERR_INVALID_ARG, "an FP8 cache needs the bf16 dtype and a finite cache_scale > 0");
@@ -113,7 +115,8 @@ bool cfg_valid(const gmla_config* c) {
   if (c->d_rope % 2) return false;
   if (c->gate_mode < GMLA_GATE_CHANNEL || c->gate_mode > GMLA_GATE_HEAD_TERNARY) return false;
   if (c->gate_mode == GMLA_GATE_HEAD_TOPK && (c->gate_topk < 1 || c->gate_topk > c->n_heads)) return false;
-  if (c->cache_dtype != GMLA_CACHE_SAME && c->cache_dtype != GMLA_CACHE_FP8_E4M3) return false;
+  if (c->cache_dtype < GMLA_CACHE_SAME || c->cache_dtype > GMLA_CACHE_FP8_BLOCK) return false;
+  if (c->cache_dtype == GMLA_CACHE_FP8_BLOCK && c->dtype != GMLA_BF16) return false;
   if (c->cache_dtype == GMLA_CACHE_FP8_E4M3 &&
       (c->dtype != GMLA_BF16 || !(c->cache_scale > 0.f) || !std::isfinite(c->cache_scale)))
     return false;
@@ -149,9 +152,18 @@ gmla_status check_cache(const gmla_config* c, const gmla_cache* k) {
     const bool ok = (ps < 128) ? (ps >= 8 && (128 % ps) == 0) : (ps % 128 == 0);
     if (!ok) return fail(GMLA_ERR_UNSUPPORTED, "page_size %d: must divide 128 (>= 8) or be a multiple of 128", ps);
   }
-  (void)c;
+  if (c->cache_dtype == GMLA_CACHE_FP8_BLOCK) {
+    GMLA_TRY(check_ptr(k->scales, "cache.scales"));
+    const int sb = k->scale_block;
+    if (sb < 1 || sb > 128 || (sb & (sb - 1)))
+      return fail(GMLA_ERR_INVALID_ARG, "cache.scale_block %d: must be a power of two in [1, 128]", sb);
+    if (k->paged && k->page_size % sb)
+      return fail(GMLA_ERR_INVALID_ARG, "cache.scale_block %d must divide page_size %d", sb, k->page_size);
+  }
   return GMLA_OK;
 }
+
+bool fp8_cache(const gmla_config* c) { return c->cache_dtype != GMLA_CACHE_SAME; }
 
 CacheView cache_view(const gmla_config* c, const gmla_cache* k) {
   CacheView v{};
@@ -359,7 +371,7 @@ size_t gmla_decode_workspace_size(const gmla_config* cfg, int32_t B) {
   if (!cfg_valid(cfg) || B < 0) return 256;
   if (cfg->dtype == GMLA_FP32) return 256;
   return decode_layout(B, cfg->n_heads, decode_eff_heads(cfg), cfg->d_h, cfg->d_c, cfg->d_rope, num_sms(),
-                       cfg->cache_dtype == GMLA_CACHE_FP8_E4M3).total;
+                       fp8_cache(cfg)).total;
 }
 
 size_t gmla_prefill_workspace_size(const gmla_config* cfg, int32_t T, int32_t B) {
@@ -473,6 +485,9 @@ gmla_status gmla_latent_project(const gmla_config* cfg, const gmla_weights* w, c
   if (!w) return fail(GMLA_ERR_INVALID_ARG, "weights is NULL");
   if (T < 0) return fail(GMLA_ERR_INVALID_ARG, "T < 0");
   GMLA_TRY(check_cache(cfg, cache));
+  if (cfg->cache_dtype == GMLA_CACHE_FP8_BLOCK)
+    return fail(GMLA_ERR_UNSUPPORTED,
+                "a block-scaled cache is written by gmla_cache_append: project into a bf16 cache of the step's rows");
   if (!workspace || workspace_bytes < gmla_latent_project_workspace_size(cfg, T))
     return fail(GMLA_ERR_WORKSPACE, "latent_project needs %zu workspace bytes",
                 gmla_latent_project_workspace_size(cfg, T));
@@ -600,7 +615,7 @@ static gmla_status decode_impl(const gmla_config* cfg, const gmla_weights* w, co
   if (cfg->d_c != 512 || (cfg->d_rope != 0 && cfg->d_rope != 64))
     return fail(GMLA_ERR_UNSUPPORTED, "bf16 decode covers d_c = 512 with d_rope in {0, 64}");
   if (cfg->d_h != 128 && cfg->d_h != 256) return fail(GMLA_ERR_UNSUPPORTED, "bf16 decode covers d_h in {128, 256}");
-  const bool fp8 = cfg->cache_dtype == GMLA_CACHE_FP8_E4M3;
+  const bool fp8 = fp8_cache(cfg);
   if (fp8 && (cfg->d_rope != 0 || cfg->d_c != 512))
     return fail(GMLA_ERR_UNSUPPORTED, "an FP8 cache covers NoPE decode with d_c = 512");
   const DecodeLayout L = decode_layout(B, cfg->n_heads, decode_eff_heads(cfg), cfg->d_h, cfg->d_c, cfg->d_rope,
@@ -679,6 +694,11 @@ static gmla_status decode_impl(const gmla_config* cfg, const gmla_weights* w, co
   a.partial_out = partial_out;
   a.fp8 = fp8 ? 1 : 0;
   a.cache_scale = cfg->cache_scale;
+  if (cfg->cache_dtype == GMLA_CACHE_FP8_BLOCK) {
+    a.cache_scale = 1.f;
+    a.scales = cache->scales;
+    while ((1 << a.scale_shift) < cache->scale_block) ++a.scale_shift;
+  }
   a.qmul = reinterpret_cast<float*>(ws + L.off_qmul);
   a.olat = ws + L.off_olat;
   const SwapPlan& sp = L.gemm_plan;
@@ -819,7 +839,7 @@ gmla_status gmla_prefill(const gmla_config* cfg, const gmla_weights* w, const vo
   if (B == 0 || T == 0) return GMLA_OK;
   if (B > cache->batch) return fail(GMLA_ERR_INVALID_ARG, "B (%d) exceeds cache.batch (%d)", B, cache->batch);
   if (cache->paged) return fail(GMLA_ERR_UNSUPPORTED, "prefill reads a contiguous cache");
-  if (cfg->cache_dtype == GMLA_CACHE_FP8_E4M3)
+  if (fp8_cache(cfg))
     return fail(GMLA_ERR_UNSUPPORTED, "prefill reads a bf16 or fp32 cache (an FP8 cache is read by decode)");
   if (max_seqlen > cache->capacity) return fail(GMLA_ERR_INVALID_ARG, "max_seqlen exceeds cache.capacity");
   GMLA_TRY(check_ptr(q, "q"));
@@ -927,6 +947,40 @@ gmla_status gmla_prefill(const gmla_config* cfg, const gmla_weights* w, const vo
 }
 
 // ---------------------------------------------------------------------------
+// y [T, d_model] = src [T, H*d_h] W^T on the tensor-core GEMM (bf16). weights_written: W
+// comes from an earlier kernel of the stream.
+static gmla_status out_gemm(const gmla_config* cfg, const void* src, int T, const void* W, bool weights_written,
+                            void* y, int* status, cudaStream_t st, const char* name) {
+  const int HD = cfg->n_heads * cfg->d_h, dm = cfg->d_model;
+  if (HD % 8) return fail(GMLA_ERR_UNSUPPORTED, "bf16 path needs H*d_h %% 8 == 0");
+  const EpiSeg ep = plain_seg(y, dm, 1 << 30, 0, 0, false, nullptr, false, false);
+  GemmArgs a{};
+  const bool swap = T <= 256;
+  const SwapPlan sp = gemm_swap_plan((dm + 127) / 128, T, HD, num_sms());
+  const int bn = swap ? sp.bn : 256;
+  const int wtile = gemm_weight_tile(swap, bn);
+  if (!make_tmap_2d(&a.act, src, HD, T, static_cast<uint64_t>(HD) * 2, 64, swap ? bn : 128, true) ||
+      !make_tmap_2d(&a.wt[0], W, HD, dm, static_cast<uint64_t>(HD) * 2, 64, wtile, true))
+    return fail(GMLA_ERR_CUDA, "tensor maps for %s failed", name);
+  a.epi[0] = ep;
+  a.seg_rows[0] = dm;
+  a.seg_tile_begin[0] = 0;
+  a.seg_tile_begin[1] = (dm + wtile - 1) / wtile;
+  a.n_seg = 1;
+  a.T = T;
+  a.K = HD;
+  a.row_mode = 0;
+  a.weights_written = weights_written ? 1 : 0;
+  a.status = status;
+  const int ttiles = swap ? sp.ttiles : (T + 127) / 128;
+  if (swap) {
+    a.splits = sp.splits;
+    a.kb_per_split = sp.kb_per_split;
+  }
+  cudaError_t e = launch_gemm_bf16(a, swap, bn, ttiles, st, "gemm_out");
+  return e == cudaSuccess ? GMLA_OK : cuda_fail(e, name);
+}
+
 gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w, const void* o, int32_t T,
                           const float* gate_logits, void* y, void* workspace, size_t workspace_bytes,
                           void* stream) {
@@ -968,31 +1022,209 @@ gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w, const v
     cudaError_t e = launch_gemm_f32(a, st);
     return e == cudaSuccess ? GMLA_OK : cuda_fail(e, "gate_out (fp32)");
   }
-  if (HD % 8) return fail(GMLA_ERR_UNSUPPORTED, "bf16 path needs H*d_h %% 8 == 0");
-  GemmArgs a{};
-  const bool swap = T <= 256;
-  const SwapPlan sp = gemm_swap_plan((dm + 127) / 128, T, HD, num_sms());
-  const int bn = swap ? sp.bn : 256;
-  const int wtile = gemm_weight_tile(swap, bn);
-  if (!make_tmap_2d(&a.act, src, HD, T, static_cast<uint64_t>(HD) * 2, 64, swap ? bn : 128, true) ||
-      !make_tmap_2d(&a.wt[0], w->W_o, HD, dm, static_cast<uint64_t>(HD) * 2, 64, wtile, true))
-    return fail(GMLA_ERR_CUDA, "tensor maps for gate_out failed");
-  a.epi[0] = ep;
-  a.seg_rows[0] = dm;
-  a.seg_tile_begin[0] = 0;
-  a.seg_tile_begin[1] = (dm + wtile - 1) / wtile;
-  a.n_seg = 1;
-  a.T = T;
-  a.K = HD;
-  a.row_mode = 0;
-  a.status = status;
-  const int ttiles = swap ? sp.ttiles : (T + 127) / 128;
-  if (swap) {
-    a.splits = sp.splits;
-    a.kb_per_split = sp.kb_per_split;
+  return out_gemm(cfg, src, T, w->W_o, false, y, status, st, "gate_out");
+}
+
+// ---------------------------------------------------------------------------
+// Most tokens that the 4-bit codes are multiplied with as they are.
+constexpr int kW4MaxDirect = 64;
+
+// workspace: status word, gate ⊙ o [T, K] bf16, then W expanded to bf16 [N, K] when T is large
+size_t gmla_gate_out_w4_workspace_size(const gmla_config* cfg, int32_t T) {
+  if (!cfg_valid(cfg) || T < 0) return 256;
+  const size_t HD = static_cast<size_t>(cfg->n_heads) * cfg->d_h;
+  const size_t act = align256(static_cast<size_t>(T) * HD * 2);
+  return 256 + act + (T > kW4MaxDirect ? align256(static_cast<size_t>(cfg->d_model) * HD * 2) : 0);
+}
+
+gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const void* o, int32_t T,
+                             const float* gate_logits, void* y, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  GMLA_TRY(check_cfg(cfg));
+  if (!w4) return fail(GMLA_ERR_INVALID_ARG, "w4 is NULL");
+  if (T < 0) return fail(GMLA_ERR_INVALID_ARG, "T < 0");
+  if (w4->group != 32 && w4->group != 64 && w4->group != 128)
+    return fail(GMLA_ERR_INVALID_ARG, "w4.group %d: must be 32, 64 or 128", w4->group);
+  const int64_t HD64 = static_cast<int64_t>(cfg->n_heads) * cfg->d_h;
+  if (HD64 % w4->group) return fail(GMLA_ERR_INVALID_ARG, "H*d_h must be a multiple of w4.group");
+  if (cfg->dtype != GMLA_BF16) return fail(GMLA_ERR_UNSUPPORTED, "4-bit weights cover the bf16 dtype");
+  if (cfg->d_h % 8 || HD64 > (1 << 24)) return fail(GMLA_ERR_UNSUPPORTED, "4-bit weights need d_h %% 8 == 0, H*d_h <= 2^24");
+  const size_t need = gmla_gate_out_w4_workspace_size(cfg, T);
+  if (!workspace || workspace_bytes < need)
+    return fail(GMLA_ERR_WORKSPACE, "gate_out_w4 needs %zu workspace bytes, got %zu", need, workspace_bytes);
+  GMLA_TRY(check_ptr(workspace, "workspace"));
+  if (T == 0) return GMLA_OK;
+  GMLA_TRY(check_ptr(o, "o"));
+  GMLA_TRY(check_ptr(y, "y"));
+  GMLA_TRY(check_ptr(w4->codes, "w4.codes"));
+  GMLA_TRY(check_ptr(w4->scales, "w4.scales"));
+  GMLA_TRY(check_ptr(gate_logits, "gate_logits", false));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int N = cfg->d_model, K = static_cast<int>(HD64), sms = num_sms();
+  int* status = static_cast<int*>(workspace);
+  uint8_t* act = static_cast<uint8_t*>(workspace) + 256;
+  if (T <= kW4MaxDirect) {
+    const W4Plan plan = w4_plan(N, T, K, sms);
+    W4PrepArgs p{o, gate_logits, act, T, K, cfg->n_heads, cfg->d_h, cfg->gate_mode, cfg->gate_topk};
+    W4Args a{};
+    if (!make_tmap_2d_u8(&a.wmap, w4->codes, K / 2, N, K / 2, 128, plan.rows) ||
+        !make_tmap_2d(&a.xmap, act, K, T, static_cast<uint64_t>(K) * 2, 64, 8 * plan.nt, true))
+      return fail(GMLA_ERR_CUDA, "tensor maps for gate_out_w4 failed");
+    a.scales = w4->scales;
+    a.y = y;
+    a.status = status;
+    a.T = T;
+    a.N = N;
+    a.K = K;
+    a.group = w4->group;
+    a.vec_scales = K % 256 == 0 ? 1 : 0;
+    cudaError_t e = launch_w4_prep(p, sms, st);
+    if (e == cudaSuccess) e = launch_w4_mma(a, plan, st);
+    return e == cudaSuccess ? GMLA_OK : cuda_fail(e, "gate_out_w4");
   }
-  cudaError_t e = launch_gemm_bf16(a, swap, bn, ttiles, st, "gemm_out");
-  return e == cudaSuccess ? GMLA_OK : cuda_fail(e, "gate_out");
+  uint8_t* W = act + align256(static_cast<size_t>(T) * K * 2);
+  const W4ExpandArgs x{w4->codes, w4->scales, W, N, K, w4->group};
+  cudaError_t e = launch_w4_expand(x, sms, st);
+  if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4: expand");
+  const void* src = o;
+  if (gate_logits) {
+    e = launch_gate_apply(o, gate_logits, act, T, cfg->n_heads, cfg->d_h, cfg->gate_mode, cfg->gate_topk, false, st);
+    if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4: gate");
+    src = act;
+  }
+  return out_gemm(cfg, src, T, W, true, y, status, st, "gate_out_w4");
+}
+
+// ---------------------------------------------------------------------------
+static gmla_status check_status_workspace(void* workspace, size_t bytes, const char* name) {
+  if (!workspace || bytes < 256)
+    return fail(GMLA_ERR_WORKSPACE, "%s needs 256 workspace bytes, got %zu", name, workspace ? bytes : size_t(0));
+  return check_ptr(workspace, "workspace");
+}
+
+gmla_status gmla_plan_batch(const int32_t* cached_lens, const int32_t* new_lens, int32_t B,
+                            const int32_t* free_pages, int32_t n_free, int32_t page_size, int32_t* block_table,
+                            int32_t max_pages_per_seq, int32_t T, int32_t* seq_lens, int32_t* cu_seqlens,
+                            int32_t* positions, int32_t* seq_ids, int64_t* slots, int32_t* pages_used,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 0 || T < 0 || n_free < 0) return fail(GMLA_ERR_INVALID_ARG, "negative size");
+  if (page_size <= 0 || max_pages_per_seq <= 0)
+    return fail(GMLA_ERR_INVALID_ARG, "page_size and max_pages_per_seq must be > 0");
+  if (static_cast<int64_t>(page_size) * max_pages_per_seq > (int64_t(1) << 31) - 1)
+    return fail(GMLA_ERR_UNSUPPORTED, "a sequence of more than 2^31 - 1 rows");
+  GMLA_TRY(check_status_workspace(workspace, workspace_bytes, "plan_batch"));
+  GMLA_TRY(check_ptr(cached_lens, "cached_lens", B > 0));
+  GMLA_TRY(check_ptr(new_lens, "new_lens", B > 0));
+  GMLA_TRY(check_ptr(free_pages, "free_pages", n_free > 0));
+  GMLA_TRY(check_ptr(block_table, "block_table", B > 0));
+  GMLA_TRY(check_ptr(seq_lens, "seq_lens", B > 0));
+  GMLA_TRY(check_ptr(cu_seqlens, "cu_seqlens"));
+  GMLA_TRY(check_ptr(positions, "positions", T > 0));
+  GMLA_TRY(check_ptr(seq_ids, "seq_ids", T > 0));
+  GMLA_TRY(check_ptr(slots, "slots", T > 0));
+  GMLA_TRY(check_ptr(pages_used, "pages_used"));
+  PlanArgs a{};
+  a.cached = cached_lens;
+  a.fresh = new_lens;
+  a.free_pages = free_pages;
+  a.table = block_table;
+  a.seq_lens = seq_lens;
+  a.cu = cu_seqlens;
+  a.positions = positions;
+  a.seq_ids = seq_ids;
+  a.slots = slots;
+  a.pages_used = pages_used;
+  a.status = static_cast<int*>(workspace);
+  a.B = B;
+  a.n_free = n_free;
+  a.page = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.T = T;
+  cudaError_t e = launch_plan_batch(a, num_sms(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GMLA_OK : cuda_fail(e, "plan_batch");
+}
+
+// ---------------------------------------------------------------------------
+gmla_status gmla_add_rms_norm(int32_t dtype, const void* x, int64_t x_stride, const void* residual,
+                              int64_t residual_stride, const void* weight, float eps, int32_t T, int32_t d,
+                              void* residual_out, int64_t residual_out_stride, void* out, int64_t out_stride,
+                              void* codes, float* scales, int32_t group, void* stream) {
+  if (dtype != GMLA_BF16 && dtype != GMLA_FP32) return fail(GMLA_ERR_INVALID_ARG, "dtype");
+  if (T < 0 || d <= 0) return fail(GMLA_ERR_INVALID_ARG, "T < 0 or d <= 0");
+  if (d > kNormMaxD) return fail(GMLA_ERR_UNSUPPORTED, "add_rms_norm covers d <= %d", kNormMaxD);
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GMLA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (group != 0 && group != 32 && group != 64 && group != 128 && group != 256)
+    return fail(GMLA_ERR_INVALID_ARG, "group %d: must be 0, 32, 64, 128 or 256", group);
+  if (T == 0) return GMLA_OK;   // (empty outputs may be NULL)
+  if ((group != 0) != (codes != nullptr) || (group != 0) != (scales != nullptr))
+    return fail(GMLA_ERR_INVALID_ARG, "codes and scales go with a group > 0");
+  if (!out && !residual_out && !codes) return fail(GMLA_ERR_INVALID_ARG, "no output is given");
+  GMLA_TRY(check_ptr(x, "x"));
+  GMLA_TRY(check_ptr(residual, "residual", false));
+  GMLA_TRY(check_ptr(weight, "weight", false));
+  GMLA_TRY(check_ptr(residual_out, "residual_out", false));
+  GMLA_TRY(check_ptr(out, "out", false));
+  GMLA_TRY(check_ptr(codes, "codes", false));
+  GMLA_TRY(check_ptr(scales, "scales", false));
+  const struct { const void* p; int64_t s; } rows[4] = {
+      {x, x_stride}, {residual, residual_stride}, {residual_out, residual_out_stride}, {out, out_stride}};
+  bool vec = d % 8 == 0;
+  for (const auto& r : rows) {
+    if (!r.p) continue;
+    if (r.s < d && T > 1) return fail(GMLA_ERR_INVALID_ARG, "a row stride is smaller than d");
+    vec = vec && (T == 1 || r.s % (dtype == GMLA_FP32 ? 4 : 8) == 0);
+  }
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.residual_out = residual_out;
+  a.out = out;
+  a.codes = static_cast<uint8_t*>(codes);
+  a.scales = scales;
+  a.x_stride = x_stride;
+  a.residual_stride = residual_stride;
+  a.residual_out_stride = residual_out_stride;
+  a.out_stride = out_stride;
+  a.T = T;
+  a.d = d;
+  a.group = group;
+  a.vec = vec ? 1 : 0;
+  a.eps = eps;
+  cudaError_t e = launch_add_rms_norm(a, dtype == GMLA_FP32, num_sms(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GMLA_OK : cuda_fail(e, "add_rms_norm");
+}
+
+// ---------------------------------------------------------------------------
+gmla_status gmla_cache_append(const gmla_config* cfg, const gmla_cache* cache, const void* latents,
+                              int64_t latent_stride, const int32_t* cu_seqlens, const int32_t* seq_lens, int32_t B,
+                              int32_t T, void* workspace, size_t workspace_bytes, void* stream) {
+  GMLA_TRY(check_cfg(cfg));
+  if (B < 0 || T < 0) return fail(GMLA_ERR_INVALID_ARG, "negative size");
+  GMLA_TRY(check_cache(cfg, cache));
+  if (cfg->cache_dtype != GMLA_CACHE_FP8_BLOCK || cfg->d_rope != 0 || cfg->d_c != 512)
+    return fail(GMLA_ERR_UNSUPPORTED, "cache_append covers a GMLA_CACHE_FP8_BLOCK cache, NoPE, d_c = 512");
+  if (latent_stride < cfg->d_c || latent_stride % 8)
+    return fail(GMLA_ERR_INVALID_ARG, "latent_stride must be >= d_c and a multiple of 8");
+  GMLA_TRY(check_status_workspace(workspace, workspace_bytes, "cache_append"));
+  if (B == 0 || T == 0) return GMLA_OK;
+  if (B > cache->batch) return fail(GMLA_ERR_INVALID_ARG, "B (%d) exceeds cache.batch (%d)", B, cache->batch);
+  GMLA_TRY(check_ptr(latents, "latents"));
+  GMLA_TRY(check_ptr(cu_seqlens, "cu_seqlens"));
+  GMLA_TRY(check_ptr(seq_lens, "seq_lens"));
+  AppendArgs a{};
+  a.latents = latents;
+  a.stride = latent_stride;
+  a.cu = cu_seqlens;
+  a.seq_lens = seq_lens;
+  a.scales = cache->scales;
+  a.cache = cache_view(cfg, cache);
+  a.status = static_cast<int*>(workspace);
+  a.B = B;
+  a.T = T;
+  a.scale_block = cache->scale_block;
+  cudaError_t e = launch_cache_append(a, num_sms(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GMLA_OK : cuda_fail(e, "cache_append");
 }
 
 }  // extern "C"

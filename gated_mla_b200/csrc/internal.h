@@ -102,6 +102,9 @@ struct DecodeArgs {
   int32_t fp8;
   float cache_scale;
   float* qmul;               // workspace: [B, H] sigma * cache_scale
+  // FP8 cache with one scale for every block of 2^scale_shift rows (null: one scale for the cache)
+  const float* scales;       // contiguous: [batch, ceil(capacity / block)]; paged: [num_pages, page_size / block]
+  int32_t scale_shift;
 };
 
 // Cross-rank merge of context-parallel partials into O_lat (bf16 [H, B, d_c]),
@@ -179,6 +182,86 @@ struct PrefillArgs {
   float scale_log2;
 };
 cudaError_t launch_prefill_attn_bf16(const PrefillArgs& a, cudaStream_t st);
+
+// ----- batch plan (plan.cu) -----
+struct PlanArgs {
+  const int32_t* cached;     // [B] rows each sequence holds
+  const int32_t* fresh;      // [B] tokens it gets
+  const int32_t* free_pages; // [n_free]
+  int32_t* table;            // [B, max_pages], in and out
+  int32_t* seq_lens;         // [B]
+  int32_t* cu;               // [B + 1]
+  int32_t* positions;        // [T]
+  int32_t* seq_ids;          // [T]
+  int64_t* slots;            // [T]
+  int32_t* pages_used;       // [1]
+  int* status;
+  int32_t B, n_free, page, max_pages, T;
+};
+cudaError_t launch_plan_batch(const PlanArgs& a, int num_sms, cudaStream_t st);
+
+// ----- residual add and root-mean-square norm (norm.cu) -----
+struct NormArgs {
+  const void* x;             // [T, d], row strides in elements
+  const void* residual;      // or null
+  const void* weight;        // [d] or null
+  void* residual_out;        // or null
+  void* out;                 // or null
+  uint8_t* codes;            // [T, d] or null
+  float* scales;             // [T, ceil(d / group)]
+  int64_t x_stride, residual_stride, residual_out_stride, out_stride;
+  int32_t T, d, group;       // group 0: no codes
+  int32_t vec;               // 16-byte accesses: d and every stride allow them
+  int32_t warps;             // warps a row (set by the launch)
+  float eps;
+};
+cudaError_t launch_add_rms_norm(NormArgs a, bool f32, int num_sms, cudaStream_t st);
+int norm_vectors(int d, int T, int num_sms);
+constexpr int kNormMaxD = 32768;   // 32 warps of 4 vectors
+
+// ----- append to a block-scaled FP8 cache (append.cu) -----
+struct AppendArgs {
+  const void* latents;       // [T, 512] bf16
+  int64_t stride;            // elements
+  const int32_t* cu;         // [B + 1]
+  const int32_t* seq_lens;   // [B], the new rows included
+  float* scales;
+  CacheView cache;
+  int* status;
+  int32_t B, T, scale_block;
+  int32_t window;            // token rows a unit looks through (set by the launch)
+};
+cudaError_t launch_cache_append(AppendArgs a, int num_sms, cudaStream_t st);
+
+// ----- product with 4-bit weights (w4.cu) -----
+struct W4PrepArgs {
+  const void* o;             // [T, K] bf16
+  const float* gate_logits;  // [T, G] or null
+  void* out;                 // [T, K] bf16
+  int32_t T, K, H, d_h, gate_mode, gate_topk;
+};
+struct W4Args {
+  CUtensorMap wmap;          // 2D [N, K / 2] bytes
+  CUtensorMap xmap;          // 2D [T, K] bf16, runs of 8 permuted
+  const void* scales;        // [N, K / group] bf16
+  void* y;                   // [T, N] bf16
+  int* status;
+  int32_t T, N, K, group;
+  int32_t vec_scales;        // the scales of a 256-k chunk are one aligned load
+};
+struct W4ExpandArgs {
+  const void* codes;
+  const void* scales;
+  void* out;                 // [N, K] bf16
+  int32_t N, K, group;
+};
+struct W4Plan {
+  int nt, mt, rows, splits;
+};
+W4Plan w4_plan(int N, int T, int K, int num_sms);
+cudaError_t launch_w4_prep(const W4PrepArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_w4_mma(const W4Args& a, const W4Plan& p, cudaStream_t st);
+cudaError_t launch_w4_expand(const W4ExpandArgs& a, int num_sms, cudaStream_t st);
 
 // ----- elementwise helpers (gmla.cu) -----
 cudaError_t launch_gate_apply(const void* o, const float* g, void* out, int T, int H, int d_h, int gate_mode,

@@ -1,0 +1,213 @@
+// norm.cu — the residual's addition and the root-mean-square norm in front of a
+// layer, with an optional E4M3 output.
+//
+//   s = x + r (fp32; s = x without a residual)          residual_out = s
+//   y = s / sqrt(mean(s^2) + eps) * w                    out = y
+//   codes = E4M3(y / scale_g), scale_g = max |y| over the group / 448 (1 for a group of zeros)
+//
+// Sums, the norm and the scale stay in fp32; s and y are rounded once, when they
+// are stored, and y is formed from the unrounded s.
+//
+// Bound by HBM: each element is read and written once. A row is held in
+// registers between the two passes (mean, then scaling), 8 consecutive elements a
+// thread and vector, so a group of 32 .. 256 elements is 4 .. 32 neighbouring
+// lanes and its maximum needs shuffles only.
+#include "common.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace gmla {
+
+namespace {
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]);
+
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, int n, bool vec, float (&v)[8]) {
+  if (vec) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? __bfloat162float(p[i]) : 0.f;
+  }
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, int n, bool vec, float (&v)[8]) {
+  if (vec) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.f;
+  }
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, int n, bool vec, const float (&v)[8]) {
+  if (vec) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = __float2bfloat16_rn(v[i]);
+  }
+}
+__device__ __forceinline__ void store8(float* p, int n, bool vec, const float (&v)[8]) {
+  if (vec) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+
+}  // namespace
+
+// One row per `warps` warps; VPT vectors of 8 elements a thread (vector i of lane t
+// covers elements 8 (i * 32 * warps + t) ..). blockDim = warps * 32 * rows a block.
+template <typename T, int VPT>
+__global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a) {
+  __shared__ float s_sum[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tpr = a.warps * 32;
+  const int lane_r = threadIdx.x % tpr;
+  const int warp0 = threadIdx.x / tpr * a.warps;      // first warp of this row in the block
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
+  const bool live = row < a.T;
+  const bool vec = a.vec != 0;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  const T* r = static_cast<const T*>(a.residual) + row * a.residual_stride;
+  T* ro = static_cast<T*>(a.residual_out) + row * a.residual_out_stride;
+  T* out = static_cast<T*>(a.out) + row * a.out_stride;
+  float v[VPT][8];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int e = (i * tpr + lane_r) * 8;
+    const int n = live ? min(8, a.d - e) : 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    if (n > 0) {
+      load8<T>(x + e, n, vec, v[i]);
+      if (a.residual) {
+        float u[8];
+        load8<T>(r + e, n, vec, u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += u[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int e = (i * tpr + lane_r) * 8;
+    const int n = live ? min(8, a.d - e) : 0;
+    if (n > 0 && a.residual_out) store8(ro + e, n, vec, v[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (a.warps > 1) {
+    const int w = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) s_sum[w] = sum;
+    __syncthreads();
+    sum = 0.f;
+    for (int i = 0; i < a.warps; ++i) sum += s_sum[warp0 + i];
+  }
+  const float inv = rsqrtf(sum / static_cast<float>(a.d) + a.eps);
+  const T* wt = static_cast<const T*>(a.weight);
+  const int g8 = a.group >> 3;           // lanes a group spans
+  const int n_group = a.group ? (a.d + a.group - 1) / a.group : 0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int e = (i * tpr + lane_r) * 8;
+    const int n = live ? min(8, a.d - e) : 0;
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = v[i][j] * inv;
+    if (n > 0 && wt) {
+      float w8[8];
+      load8<T>(wt + e, n, vec, w8);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] *= w8[j];
+    }
+    if (n > 0 && a.out) store8(out + e, n, vec, y);
+    if (a.group) {
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, j < n ? fabsf(y[j]) : 0.f);
+      for (int o = 1; o < g8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (n > 0) {
+        const float part = top / 448.f;              // 0 for a group of zeros (or of values too small to divide)
+        const float scale = part > 0.f ? part : 1.f;
+        const float mul = 1.f / scale;
+        if ((threadIdx.x & (g8 - 1)) == 0) a.scales[row * n_group + e / a.group] = scale;
+        uint8_t* c = a.codes + row * a.d + e;
+        // a scale below fp32's normal range has no finite reciprocal: divide there
+        const bool div = !(mul < 3.0e38f);
+        uint32_t w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float q[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) q[j] = div ? y[4 * h + j] / scale : y[4 * h + j] * mul;
+          w[h] = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3) |
+                 (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3))
+                  << 16);
+        }
+        if (vec) {
+          *reinterpret_cast<uint2*>(c) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < n) c[j] = static_cast<uint8_t>(w[j >> 2] >> (8 * (j & 3)));
+        }
+      }
+    }
+  }
+}
+
+template <typename T>
+static cudaError_t launch_norm(const NormArgs& a, int vpt, dim3 grid, dim3 block, cudaStream_t st) {
+  switch (vpt) {
+    case 1: return launch_pdl(add_rms_norm_kernel<T, 1>, grid, block, 0, st, 1, a);
+    case 2: return launch_pdl(add_rms_norm_kernel<T, 2>, grid, block, 0, st, 1, a);
+    default: return launch_pdl(add_rms_norm_kernel<T, 4>, grid, block, 0, st, 1, a);
+  }
+}
+
+cudaError_t launch_add_rms_norm(NormArgs a, bool f32, int num_sms, cudaStream_t st) {
+  const int nvec = (a.d + 7) / 8;
+  const int vpt = norm_vectors(a.d, a.T, num_sms);
+  a.warps = (nvec + 32 * vpt - 1) / (32 * vpt);
+  const int rows = a.warps >= 8 ? 1 : 8 / a.warps;       // rows a block (256 threads or one row)
+  const dim3 block(a.warps * 32 * rows);
+  const dim3 grid((a.T + rows - 1) / rows);
+  prof_begin(st, "add_rms_norm");
+  cudaError_t e = f32 ? launch_norm<float>(a, vpt, grid, block, st) : launch_norm<__nv_bfloat16>(a, vpt, grid, block, st);
+  prof_end(st);
+  return e;
+}
+
+// Vectors a thread: 1 where the rows are few (the shortest chain: every element's
+// load is in flight at once), more where they are many, so that a block is small
+// and an SM holds several rows in different phases.
+int norm_vectors(int d, int T, int num_sms) {
+  const int nvec = (d + 7) / 8;
+  if (nvec > 2048) return 4;
+  if (nvec > 1024) return 2;
+  if (T <= 2 * num_sms) return 1;
+  return nvec > 256 ? 4 : (nvec > 64 ? 2 : 1);
+}
+
+}  // namespace gmla

@@ -80,8 +80,18 @@ typedef enum gmla_dtype { GMLA_BF16 = 0, GMLA_FP32 = 1 } gmla_dtype;
  * blog (zwxr.cn) §7 warns that quantisation errors compound, and the library
  * keeps every other operand near bf16 precision. bf16 dtype only: decode
  * (NoPE, d_c = 512) reads it and gmla_latent_project writes it; gmla_prefill
- * over an FP8 cache returns GMLA_ERR_UNSUPPORTED. */
-typedef enum gmla_cache_dtype { GMLA_CACHE_SAME = 0, GMLA_CACHE_FP8_E4M3 = 1 } gmla_cache_dtype;
+ * over an FP8 cache returns GMLA_ERR_UNSUPPORTED.
+ * GMLA_CACHE_FP8_BLOCK: E4M3 codes with one fp32 scale for every block of
+ * cache->scale_block token rows (cache->scales; cfg->cache_scale is ignored), so
+ * that the range follows the data. bf16 dtype, NoPE, d_c = 512:
+ * gmla_cache_append writes it, gmla_decode and gmla_decode_partial read it;
+ * gmla_latent_project and gmla_prefill return GMLA_ERR_UNSUPPORTED (project into a
+ * bf16 cache of the step's rows and append those). */
+typedef enum gmla_cache_dtype {
+  GMLA_CACHE_SAME = 0,
+  GMLA_CACHE_FP8_E4M3 = 1,
+  GMLA_CACHE_FP8_BLOCK = 2
+} gmla_cache_dtype;
 
 /* Per-channel gate: G = H*d_h ("Gated MLA 计算公式" §二 boxed equation).
  * Per-head gate:    G = H, broadcast over the head's d_h channels
@@ -151,7 +161,23 @@ typedef struct gmla_cache {
   int32_t num_pages;          /* paged: pages in the pool */
   int32_t max_pages_per_seq;  /* paged: row length of block_table */
   const int32_t* block_table; /* paged: [batch, max_pages_per_seq] */
+  /* read under GMLA_CACHE_FP8_BLOCK only: one scale for each block of scale_block rows
+   * (a power of two <= 128, paged: a divisor of page_size), a stored code e means
+   * scale * e. contiguous: [batch, ceil(capacity / scale_block)]; paged:
+   * [num_pages, page_size / scale_block]. Scales of blocks that hold rows lie in
+   * [2^-32, 2^32]; one outside (or NaN) sets GMLA_ERR_DEVICE_RANGE in a decode. */
+  float* scales;
+  int32_t scale_block;
 } gmla_cache;
+
+/* A weight matrix in 4 bits: codes [N, K/2] (two per byte, even k in the low
+ * nibble), scales [N, K/group] bf16, group 32, 64 or 128:
+ * W[n, k] = (code - 8) * scales[n, k / group]. */
+typedef struct gmla_w4 {
+  const void* codes;
+  const void* scales;
+  int32_t group;
+} gmla_w4;
 
 /* ---------------------------------------------------------------------------
  * gmla_latent_project — everything computed from the tokens' own hidden states.
@@ -227,6 +253,95 @@ GMLA_API gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w
                           const void* o, int32_t T, const float* gate_logits,
                           void* y, void* workspace, size_t workspace_bytes,
                           void* stream);
+
+/* ---------------------------------------------------------------------------
+ * gmla_gate_out_w4 — gmla_gate_out with W_o held in 4 bits:
+ *   y[t, n] = sum_g scales[n, g] * sum_{k in g} (code[n, k] - 8) (gate ⊙ o)[t, k]
+ *   w4           W_o as [d_model, H*d_h] (H*d_h a multiple of the group)
+ *   o, T, gate_logits, y: as gmla_gate_out (bf16 dtype only)
+ *   workspace    gmla_gate_out_w4_workspace_size(cfg, T) bytes; calls that may
+ *                overlap need workspaces of their own
+ * Up to 64 tokens the codes are multiplied as they are (no weight is rounded);
+ * above that they are expanded to bf16 in the workspace once a call, which rounds
+ * each weight once.
+ * ------------------------------------------------------------------------- */
+GMLA_API gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4,
+                                      const void* o, int32_t T, const float* gate_logits,
+                                      void* y, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+GMLA_API size_t gmla_gate_out_w4_workspace_size(const gmla_config* cfg, int32_t T);
+
+/* ---------------------------------------------------------------------------
+ * gmla_plan_batch — what one step of a batch over a paged cache needs, made on
+ * the GPU from its request lengths: pages for the new rows, and for every new
+ * token its position, its sequence and its row of the page pool.
+ *   cached_lens  [B] int32: rows each sequence holds already
+ *   new_lens     [B] int32: tokens each sequence gets in this step (0 is allowed)
+ *   free_pages   [n_free] int32: unused page ids; the first *pages_used are taken,
+ *                in the order of the sequences
+ *   block_table  [B, max_pages_per_seq] int32, in and out: entries of the pages that
+ *                a sequence's new rows begin are written, all others are left as they were
+ *   T            token rows of the outputs (>= the sum of new_lens)
+ *   seq_lens     [B] = cached + new;  cu_seqlens [B+1] = prefix sums of new_lens
+ *   positions, seq_ids [T] int32, slots [T] int64: packed by sequence; slot = page *
+ *                page_size + row. Rows behind the last sequence's get -1 in all three
+ *   pages_used   [1] int32
+ *   workspace    256 bytes (the status word)
+ * A batch that cannot be (a negative length, a sequence beyond max_pages_per_seq pages,
+ * more tokens than T, fewer free pages than needed) sets GMLA_ERR_DEVICE_RANGE and is
+ * planned as empty: lengths, offsets and pages_used 0, every token row -1, the
+ * block table untouched. A negative page id sets it too and gives slot -1.
+ * ------------------------------------------------------------------------- */
+GMLA_API gmla_status gmla_plan_batch(const int32_t* cached_lens, const int32_t* new_lens, int32_t B,
+                                     const int32_t* free_pages, int32_t n_free, int32_t page_size,
+                                     int32_t* block_table, int32_t max_pages_per_seq, int32_t T,
+                                     int32_t* seq_lens, int32_t* cu_seqlens, int32_t* positions,
+                                     int32_t* seq_ids, int64_t* slots, int32_t* pages_used,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * gmla_add_rms_norm — the residual's addition and the root-mean-square norm in
+ * front of a layer, with an optional output in 8 bits:
+ *   s = x + residual;  y = s / sqrt(mean(s^2) + eps) * weight
+ *   dtype        of x, residual, weight, residual_out, out (gmla_dtype); the
+ *                arithmetic is fp32, s and y are rounded once, when stored
+ *   x            [T, d] (d <= 32768), rows x_stride elements apart, likewise the others
+ *   residual     or NULL (s = x);  weight [d] or NULL (all ones)
+ *   residual_out gets s, or NULL; may be `residual` or `x` itself
+ *   out          gets y, or NULL; may be `x` itself
+ *   codes        [T, d] E4M3 codes of y / scale (round to nearest even), with
+ *   scales       [T, ceil(d / group)] fp32: max |y| over the group / 448, 1 for a group of
+ *                zeros; group 32, 64, 128 or 256. Both NULL with group = 0: no 8-bit output
+ * A row with a NaN or an infinity gives NaN in y and undefined codes.
+ * ------------------------------------------------------------------------- */
+GMLA_API gmla_status gmla_add_rms_norm(int32_t dtype, const void* x, int64_t x_stride,
+                                       const void* residual, int64_t residual_stride,
+                                       const void* weight, float eps, int32_t T, int32_t d,
+                                       void* residual_out, int64_t residual_out_stride,
+                                       void* out, int64_t out_stride,
+                                       void* codes, float* scales, int32_t group, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * gmla_cache_append — the new latent rows of a step into a GMLA_CACHE_FP8_BLOCK cache.
+ *   latents      [T, d_c] bf16, packed by sequence, rows latent_stride elements apart
+ *                (a multiple of 8)
+ *   cu_seqlens   [B+1] int32: sequence b's new rows are cu_seqlens[b] .. cu_seqlens[b+1]-1,
+ *                cu_seqlens[0] = 0; rows from cu_seqlens[B] on are not read
+ *   seq_lens     [B] int32: rows of each sequence INCLUDING the new ones, which go to
+ *                positions seq_lens[b] - n_b .. seq_lens[b] - 1
+ * A block's scale is 2^E with the smallest E in [-32, 32] for which no row of the
+ * block exceeds 448 * 2^E. A block that holds rows already keeps the larger of its
+ * scale and that one; when it grows, the held codes are rounded again to the new
+ * scale. Rows of other blocks, and rows behind the new ones, are left as they were.
+ * Sequences must not share the pages that they write. A length or page out of range
+ * sets GMLA_ERR_DEVICE_RANGE and its rows are skipped.
+ *   workspace    256 bytes (the status word)
+ * ------------------------------------------------------------------------- */
+GMLA_API gmla_status gmla_cache_append(const gmla_config* cfg, const gmla_cache* cache,
+                                       const void* latents, int64_t latent_stride,
+                                       const int32_t* cu_seqlens, const int32_t* seq_lens,
+                                       int32_t B, int32_t T, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * gmla_decode_noalloc — gmla_decode for callers that cannot allocate device
