@@ -77,20 +77,24 @@ class LatentCache:
 
 
 def _check(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> None:
-    """A tensor argument of the calls below: its type, its sizes (None: any) and its device."""
-    if t.dtype != dtype or t.device != device or t.dim() != len(shape) or any(
-            n is not None and n != m for n, m in zip(shape, t.shape)):
+    """A tensor argument of the calls below: its type, its sizes and its device."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+# the current stream's handle without a Stream object around it (3 us less a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _stream_of(t: torch.Tensor) -> int:
     """The current stream, which has to be one of the tensor's device."""
     if not t.is_cuda:
         raise ValueError("gated_mla_b200 takes CUDA tensors only")
-    if t.device.index != torch.cuda.current_device():
+    index = t.get_device()
+    if index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}: "
                          "call inside torch.cuda.device(...)")
-    return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(index)
 
 
 class _Scratch:
@@ -101,6 +105,7 @@ class _Scratch:
         self._held = {}
 
     def get(self, key: str, nbytes: int, device: torch.device, stream: int) -> torch.Tensor:
+        """At least `nbytes` bytes whose status word was zeroed when they were made."""
         capturing = torch.cuda.is_current_stream_capturing()
         ws = None if capturing else self._held.get((key, device.index, stream))
         if ws is None or ws.numel() < nbytes:
@@ -150,22 +155,25 @@ def plan_batch(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     i32 = torch.int32
     _check(cached_lens, "cached_lens", i32, (B,), dev)
     _check(new_lens, "new_lens", i32, (B,), dev)
-    _check(block_table, "block_table", i32, (B, None), dev)
-    _check(free_pages, "free_pages", i32, (None,), dev)
-    if T < 0:
-        raise ValueError("n_tokens must be >= 0")
+    if block_table.dim() != 2 or free_pages.dim() != 1 or T < 0:
+        raise ValueError("block_table is [B, max_pages], free_pages [n], n_tokens >= 0")
+    M, n_free = block_table.shape[1], free_pages.shape[0]
+    _check(block_table, "block_table", i32, (B, M), dev)
+    _check(free_pages, "free_pages", i32, (n_free,), dev)
     if out is None:
         new = lambda n, t=i32: torch.empty(n, dtype=t, device=dev)  # noqa: E731
         out = BatchPlan(new(B), new(B + 1), new(T), new(T), new(T, torch.int64), new(1))
     else:
-        for name, n, t in (("seq_lens", B, i32), ("cu_seqlens", B + 1, i32), ("positions", T, i32), ("seq_ids", T, i32),
-                           ("slots", T, torch.int64), ("pages_used", 1, i32)):
-            _check(getattr(out, name), "out." + name, t, (n,), dev)
+        _check(out.seq_lens, "out.seq_lens", i32, (B,), dev)
+        _check(out.cu_seqlens, "out.cu_seqlens", i32, (B + 1,), dev)
+        _check(out.positions, "out.positions", i32, (T,), dev)
+        _check(out.seq_ids, "out.seq_ids", i32, (T,), dev)
+        _check(out.slots, "out.slots", torch.int64, (T,), dev)
+        _check(out.pages_used, "out.pages_used", i32, (1,), dev)
     ws = _scratch.get("plan_batch", 256, dev, stream)
-    L.check(L.gmla_plan_batch(_p(cached_lens), _p(new_lens), B, _p(free_pages), free_pages.shape[0], int(page_size),
-                              _p(block_table), block_table.shape[1], T, _p(out.seq_lens), _p(out.cu_seqlens),
-                              _p(out.positions), _p(out.seq_ids), _p(out.slots), _p(out.pages_used), ws.data_ptr(),
-                              ws.numel(), stream), "gmla_plan_batch")
+    L.check(L.gmla_plan_batch(_p(cached_lens), _p(new_lens), B, _p(free_pages), n_free, int(page_size), _p(block_table),
+                              M, T, _p(out.seq_lens), _p(out.cu_seqlens), _p(out.positions), _p(out.seq_ids),
+                              _p(out.slots), _p(out.pages_used), ws.data_ptr(), 256, stream), "gmla_plan_batch")
     return out
 
 
@@ -203,19 +211,22 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residua
             raise ValueError("fp8_group must be 0, 32, 64, 128 or 256")
         codes = torch.empty(T, d, dtype=torch.float8_e4m3fn, device=dev)
         scales = torch.empty(T, -(-d // fp8_group), dtype=torch.float32, device=dev)
-    rows = []
-    for name, t in (("x", x), ("residual", residual), ("residual_out", residual_out), ("out", out)):
+
+    def row(t, name):      # address and row stride
         if t is None:
-            rows += [None, 0]
-            continue
+            return None, 0
         _check(t, name, x.dtype, (T, d), dev)
+        if t.is_contiguous():
+            return t.data_ptr(), d
         if d > 1 and t.stride(1) != 1:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
-        rows += [t.data_ptr(), t.stride(0) if T > 1 else d]
+        return t.data_ptr(), t.stride(0) if T > 1 else d
+
     if weight is not None:
         _check(weight, "weight", x.dtype, (d,), dev)
-    L.check(L.gmla_add_rms_norm(_DT[x.dtype], *rows[:4], _p(weight), eps, T, d, *rows[4:], _p(codes), _p(scales),
-                                fp8_group, stream), "gmla_add_rms_norm")
+    L.check(L.gmla_add_rms_norm(_DT[x.dtype], *row(x, "x"), *row(residual, "residual"), _p(weight), eps, T, d,
+                                *row(residual_out, "residual_out"), *row(out, "out"), _p(codes), _p(scales), fp8_group,
+                                stream), "gmla_add_rms_norm")
     return NormOut(out, residual_out, codes, scales)
 
 
@@ -295,7 +306,7 @@ class GatedMLA:
 
     @staticmethod
     def _stream() -> int:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
 
     # -- the four calls
     @property
@@ -367,10 +378,12 @@ class GatedMLA:
         stream = _stream_of(latents)
         dev, c = latents.device, self.cfg
         B = seq_lens.shape[0]
-        _check(latents, "latents", self.dtype, (None, c.d_c), dev)
+        if latents.dim() != 2:
+            raise ValueError("latents is [T, d_c]")
+        T = latents.shape[0]
+        _check(latents, "latents", self.dtype, (T, c.d_c), dev)
         _check(seq_lens, "seq_lens", torch.int32, (B,), dev)
         _check(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
-        T = latents.shape[0]
         if latents.stride(1) != 1:
             raise ValueError("latents: the elements of a row must be contiguous")
         ws = self._scratch.get("append", 256, dev, stream)

@@ -95,6 +95,32 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// As mbar_wait, polling with the non-blocking probe only. A thread that try_wait
+// suspends is woken about a microsecond late (measured on sm_100a), which is the
+// whole time of a short pipeline stage. kSleepNs > 0 sleeps between probes: for
+// whole warps with a little slack, whose probes would otherwise crowd out those of
+// the thread that the pipeline hangs on.
+template <int kSleepNs>
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  if (mbar_test(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (kSleepNs > 0) __nanosleep(kSleepNs);
+    if (mbar_test(bar, parity)) return true;
+    if ((it & 255u) == 0) {
+      if (*abort) return false;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = t;
+      } else if (t - t0 > kWaitLimitNs) {
+        *abort = 1;
+        report_status(status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+}
+
 // As mbar_wait, with cluster-scope acquire: for barriers completed by other
 // CTAs of the cluster (st.async transactions).
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
@@ -311,6 +337,28 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_u32(bar))
                : "memory");
+}
+
+// MMA and commit by a whole converged warp, of which one elected lane issues: the
+// operands stay in uniform registers (a lone lane moves each of them there first,
+// which costs more than the MMA of a small tile).
+// A (M rows in lanes, two bf16 per 32-bit column) is read from tensor memory.
+__device__ __forceinline__ void umma_bf16_ta_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                  uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_warp(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar))
+      : "memory");
 }
 
 // 32 lanes x 32 bit, 16 consecutive columns per thread.

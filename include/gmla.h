@@ -261,9 +261,8 @@ GMLA_API gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w
  *   o, T, gate_logits, y: as gmla_gate_out (bf16 dtype only)
  *   workspace    gmla_gate_out_w4_workspace_size(cfg, T) bytes; calls that may
  *                overlap need workspaces of their own
- * Up to 64 tokens the codes are multiplied as they are (no weight is rounded);
- * above that they are expanded to bf16 in the workspace once a call, which rounds
- * each weight once.
+ * The codes are multiplied as they are and the scale is applied in fp32: no weight
+ * is rounded. Works for any T, from one token to whole prompts.
  * ------------------------------------------------------------------------- */
 GMLA_API gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4,
                                       const void* o, int32_t T, const float* gate_logits,
