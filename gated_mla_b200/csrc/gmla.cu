@@ -1062,7 +1062,7 @@ gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const vo
     return fail(GMLA_ERR_UNSUPPORTED, "gate_out_w4: more than 2^30 tiles of work");
   float* rest = reinterpret_cast<float*>(act + w4_act_bytes(plan));
   const W4PrepArgs p{o,        gate_logits,    act,            rest,      T,       K,          cfg->n_heads,
-                     cfg->d_h, cfg->gate_mode, cfg->gate_topk, w4->group, plan.T8, plan.K256, plan.nt};
+                     cfg->d_h, cfg->gate_mode, cfg->gate_topk, w4->group, plan.T8, plan.K256, plan.nt, plan.bn};
   cudaError_t e = launch_w4_prep(p, sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4");
   CUtensorMap wmap;
@@ -1087,8 +1087,7 @@ gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const vo
   } else {
     W4TcArgs a{};
     a.wmap = wmap;
-    if (!make_tmap_2d(&a.xmap, act, K, T, static_cast<uint64_t>(K) * 2, 64, plan.bn, true))
-      return fail(GMLA_ERR_CUDA, "tensor map for gate_out_w4 failed");
+    a.x = act;
     a.scales = w4->scales;
     a.y = y;
     a.part = rest;

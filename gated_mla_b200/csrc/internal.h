@@ -238,10 +238,10 @@ constexpr int kW4Chunk = 256;   // k per pipeline stage
 struct W4PrepArgs {
   const void* o;             // [T, K] bf16
   const float* gate_logits;  // [T, G] or null
-  void* out;                 // [T8, K256] bf16 in fragment order
+  void* out;                 // [T8, K256] bf16 in the order the product reads
   float* sums;               // [K / group, T8]: -136 sum of the group's activations
   int32_t T, K, H, d_h, gate_mode, gate_topk, group;
-  int32_t T8, K256, nt;      // of the plan
+  int32_t T8, K256, nt, bn;  // of the plan
 };
 struct W4Args {
   CUtensorMap wmap;          // 2D [N, K / 2] bytes
@@ -255,7 +255,7 @@ struct W4Args {
 };
 struct W4TcArgs {
   CUtensorMap wmap;          // 2D [N, K / 2] bytes
-  CUtensorMap xmap;          // 2D [T, K] bf16, runs of 8 permuted
+  const void* x;             // w4_prep's out
   const void* scales;        // [N, K / group] bf16
   void* y;                   // [T, N] bf16
   float* part;               // [G, 2, BN, 128] partial tiles
@@ -272,7 +272,7 @@ struct W4Plan {
   int nt, splits;            // m16n8k16: token tiles of 8 a CTA (0: tcgen05), K splits
   int bn, G;                 // tcgen05: tokens a tile, CTAs
   int row_tiles, tok_tiles, n_chunk;
-  int T8, K256;              // m16n8k16: tokens and k rounded up to whole tiles
+  int T8, K256;              // tokens and k rounded up to whole tiles
 };
 constexpr int kW4MaxMma = 8;
 W4Plan w4_plan(int N, int T, int K, int num_sms);

@@ -105,8 +105,8 @@ namespace gmla {
 // out: [T8 / 8nt blocks][K256 / 32 steps][nt][g * 4 + c][8 bf16]: token 8 n + g of the block,
 // k = 32 step + 8 c + (0 4 1 5 2 6 3 7); sums: [n_groups][T8] fp32. Tokens and k behind
 // the end are zeros. A thread makes one run of 8 k; the runs of a group are
-// neighbouring lanes. nt = 0 (for w4_tc): out is [T, K] with each run of 8 stored as
-// 0 4 1 5 2 6 3 7, and no sums are made.
+// neighbouring lanes. nt = 0 (for w4_tc): out is the image of the swizzled shared-memory
+// tiles [T8 / bn][K256 / 64][bn][128 bytes], the runs of 8 in the same order, and no sums are made.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
   griddep_wait();
@@ -150,7 +150,9 @@ __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
     r.z = __byte_perm(w[1], w[3], 0x5410);
     r.w = __byte_perm(w[1], w[3], 0x7632);
     if (a.nt == 0) {
-      if (i < n) reinterpret_cast<uint4*>(a.out)[i] = r;
+      const int tb = t / a.bn, tn = t % a.bn;
+      const int64_t at = ((static_cast<int64_t>(tb) * (a.K256 >> 6) + (k >> 6)) * a.bn + tn) * 8 + (((k >> 3) ^ tn) & 7);
+      if (i < n) reinterpret_cast<uint4*>(a.out)[at] = r;
       continue;
     }
     float sum = 0.f;
@@ -427,8 +429,8 @@ W4Plan w4_plan(int N, int T, int K, int num_sms) {
     p.tok_tiles = (T + p.bn - 1) / p.bn;
     const int64_t U = row_tiles * p.tok_tiles * chunks;
     p.G = static_cast<int>(U < num_sms ? U : num_sms);
-    p.T8 = T;
-    p.K256 = K;
+    p.T8 = p.tok_tiles * p.bn;
+    p.K256 = chunks * kW4Chunk;
     return p;
   }
   p.nt = T <= 8 ? 1 : 2;

@@ -8,14 +8,16 @@
 //
 // Roles (one CTA per SM, each working through an equal range of 256-k chunks of the
 // row x token tiles laid end to end):
-//   * a copy warp streams code boxes (128 rows x 128 bytes = 256 k) and activation
-//     boxes (BN tokens x 64 k);
+//   * one warp streams code boxes (128 rows x 128 bytes = 256 k), another the activations
+//     (BN tokens x 128 k, stored by w4_prep as the image of the swizzled shared-memory
+//     tiles: one bulk copy). Together in one thread, with its waits, they took 950 cycles a block;
 //   * eight expanding warps: thread = row, 32 bytes of codes become 32 columns (64 k) of an A
 //     block of 128 k in tensor memory. (Through shared memory, which the MMA would read
 //     again, the kernel was bound by shared-memory bandwidth: 530 cycles for 64 k.)
-//   * one thread issues the MMAs: a group's blocks accumulate into one of two
-//     TMEM buffers;
-//   * four warps (eight at BN = 128) promote: acc += scale[row] * buffer, thread = row.
+//   * two warps issue the MMAs, of alternate blocks, into accumulators of their own: a wait on
+//     a barrier costs about 250 cycles even when it is complete, an MMA of this size 45
+//     (one issuing warp: 1040 cycles a block of 128 k);
+//   * four warps (eight from BN = 64 on) promote: acc += scale[row] * buffer, thread = row.
 // What bounds it: at BN <= 128 an MMA of M = 128, K = 16 costs a fixed 64 cycles, 256
 // cycles for 4 KB of codes, which is 0.7 of the HBM rate at few tokens and the full
 // bf16 rate at 128; the expansion (11 instructions and a 16-byte store for 8 codes) and
@@ -30,23 +32,25 @@ namespace {
 
 struct W4TcSmem {
   uint64_t code_full[4], code_empty[4];
-  uint64_t full[4], ax_empty[4];   // an A block and its activations: 256 expanding threads and the copy thread arrive
-  uint64_t d_full[2], d_free[2];
-  uint64_t drain;
+  uint64_t full[4], ax_empty[4];   // an A block and its activations: the expanding threads and a copy thread arrive
+  uint64_t d_full[4], d_free[4];
+  uint64_t drain[2];
   uint32_t tmem;
   int abort;
 };
 
 template <int BN>
 struct W4TcCfg {
-  static constexpr int kEpi = BN == 128 ? 8 : 4;               // promoting warps
+  static constexpr int kEpi = BN >= 64 ? 8 : 4;                // promoting warps
   static constexpr int kCols = BN / (kEpi / 4);                // accumulators a thread
-  static constexpr int kThreads = 32 * (2 + kEpi + 8);
+  static constexpr int kExp = BN == 128 ? 4 : 8;               // expanding warps (with 8 at BN = 128 the sums would spill)
+  static constexpr int kThreads = 32 * (4 + kEpi + kExp);
   static constexpr int kCode = 128 * 128;                      // 256 k
   static constexpr int kX = BN * 256;                          // activations of a block of 128 k: two tiles of 128-byte rows
   static constexpr int kCodeStages = 4, kStages = 3;
   static constexpr int kACols = 64;                            // TMEM columns of an A block (two bf16 each)
-  static constexpr int kTmemUsed = 2 * BN + kStages * kACols;
+  static constexpr int kBufs = BN == 128 ? 1 : 2;              // accumulators of an issuing warp
+  static constexpr int kTmemUsed = 2 * kBufs * BN + kStages * kACols;
   static constexpr int kTmem = kTmemUsed <= 256 ? 256 : 512;
   static constexpr int kSmem = kCodeStages * kCode + kStages * kX + 1024 + static_cast<int>(sizeof(W4TcSmem));
   static_assert(kTmemUsed <= 512, "tensor memory");
@@ -71,17 +75,18 @@ __global__ void __launch_bounds__(W4TcCfg<BN>::kThreads, 1) w4_tc_kernel(const _
   if (threadIdx.x == 0) {
     for (int i = 0; i < NC; ++i) {
       mbar_init(&sm->code_full[i], 1);
-      mbar_init(&sm->code_empty[i], 8);
+      mbar_init(&sm->code_empty[i], C::kExp);
     }
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&sm->full[i], 257);
+      mbar_init(&sm->full[i], 32 * C::kExp + 1);
       mbar_init(&sm->ax_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sm->d_full[i], 1);
       mbar_init(&sm->d_free[i], 32 * C::kEpi);
     }
-    mbar_init(&sm->drain, 1);
+    mbar_init(&sm->drain[0], 1);
+    mbar_init(&sm->drain[1], 1);
     sm->abort = 0;
     fence_mbar_init();
   }
@@ -93,62 +98,69 @@ __global__ void __launch_bounds__(W4TcCfg<BN>::kThreads, 1) w4_tc_kernel(const _
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const uint32_t tmem = sm->tmem;          // two accumulators of BN columns, then the A blocks
-  const uint32_t tA = tmem + 2 * BN;
+  const uint32_t tmem = sm->tmem;          // the accumulators of BN columns, then the A blocks
+  const uint32_t tA = tmem + 2 * C::kBufs * BN;
+  constexpr int GPB = 8 / MPG;             // groups a block: group g of block b is number (b >> 1) * GPB + g of its warp
   const int n_chunk = a.n_chunk;
   const int64_t U = static_cast<int64_t>(a.row_tiles) * a.tok_tiles * n_chunk;
   const int u_lo = w4_range(U, gridDim.x, blockIdx.x), u_hi = w4_range(U, gridDim.x, blockIdx.x + 1);
   const int n_u = u_hi - u_lo;
+  // the range's first tile and its first chunk there (counted up from here: a division
+  // in a thread that issues alone costs as much as a copy)
+  const int tile0 = u_lo / n_chunk, ch0 = u_lo - tile0 * n_chunk;
+  const int rt0 = tile0 / a.tok_tiles, tt0 = tile0 - rt0 * a.tok_tiles;
 
   if (warp == 0) {
-    // ------------------------------ copies ------------------------------
+    // ------------------------------ codes ------------------------------
     if (lane == 0) {
       tma_prefetch_desc(&a.wmap);
-      tma_prefetch_desc(&a.xmap);
-      const uint64_t pol_w = a.tok_tiles > 1 ? l2_evict_normal() : l2_evict_first(), pol_x = l2_evict_last();
-      auto load_w = [&](int i) {   // chunk i of the range
-        const int u = u_lo + i, tile = u / n_chunk;
-        mbar_arrive_expect_tx(&sm->code_full[i % NC], C::kCode);
-        tma_load_2d(&a.wmap, &sm->code_full[i % NC], codes + (i % NC) * C::kCode, (u % n_chunk) * 128,
-                    tile / a.tok_tiles * 128, pol_w);
-      };
+      const uint64_t pol_w = a.tok_tiles > 1 ? l2_evict_normal() : l2_evict_first();
       // the weights: the kernel before this one (w4_prep) neither writes them nor starts this
-      // one before all earlier kernels are done, so they are requested before the wait
-      int wi = 0, xi = 0;
-      for (; wi < n_u && wi < NC; ++wi) load_w(wi);
-      griddep_wait();
-      bool ok = true;
-      for (int i = 0; i < n_u && ok; ++i) {
-        const int u = u_lo + i, tile = u / n_chunk, k0 = (u % n_chunk) * kW4Chunk, t0 = tile % a.tok_tiles * BN;
-        for (int j = 0; j < 2; ++j, ++xi) {
-          const int s = xi % NS;
-          if (xi >= NS && !mbar_poll<20>(&sm->ax_empty[s], ((xi / NS) & 1) ^ 1, abort_flag, a.status)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&sm->full[s], C::kX);
-          for (int h = 0; h < 2; ++h)
-            tma_load_2d(&a.xmap, &sm->full[s], sx + s * C::kX + h * (C::kX / 2), k0 + j * 128 + h * 64, t0, pol_x);
-        }
-        if (!ok) break;
-        // the code stage that held chunk wi - NC: freed by the expanding warps, which run ahead of the MMAs
-        if (wi < n_u) {
-          if (!mbar_poll<20>(&sm->code_empty[wi % NC], ((wi / NC) & 1) ^ 1, abort_flag, a.status)) break;
-          load_w(wi++);
+      // one before all earlier kernels are done, so they are requested without a wait
+      int i = 0, ch = ch0, tt = tt0, row = rt0 * 128;
+      for (; i < n_u; ++i) {
+        const int s = i % NC;
+        if (i >= NC && !mbar_poll<20>(&sm->code_empty[s], ((i / NC) & 1) ^ 1, abort_flag, a.status)) break;
+        mbar_arrive_expect_tx(&sm->code_full[s], C::kCode);
+        tma_load_2d(&a.wmap, &sm->code_full[s], codes + s * C::kCode, ch * 128, row, pol_w);
+        if (++ch == n_chunk) {
+          ch = 0;
+          if (++tt == a.tok_tiles) tt = 0, row += 128;
         }
       }
-      if (*abort_flag) {   // let issued copies land before the block exits
-        for (int i = wi > NC ? wi - NC : 0; i < wi; ++i) mbar_drain(&sm->code_full[i % NC], (i / NC) & 1);
-        for (int i = xi > NS ? xi - NS : 0; i < xi; ++i) mbar_drain(&sm->full[i % NS], (i / NS) & 1);
-      }
+      if (*abort_flag)   // let issued copies land before the block exits
+        for (int c = i > NC ? i - NC : 0; c < i; ++c) mbar_drain(&sm->code_full[c % NC], (c / NC) & 1);
     }
-  } else if (warp == 1) {
-    // ------------------------------ MMA issuer (the whole warp, converged) ------------------------------
+  } else if (warp == 3) {
+    // ------------------------------ activations ------------------------------
+    if (lane == 0) {
+      const uint64_t pol_x = l2_evict_last();
+      griddep_wait();
+      int b = 0, s = 0, tt = tt0, left = 2 * (n_chunk - ch0);   // blocks left in the tile
+      const uint8_t* x = static_cast<const uint8_t*>(a.x);
+      const uint8_t* src = x + (static_cast<int64_t>(tt0) * n_chunk + ch0) * 2 * C::kX;
+      for (; b < 2 * n_u; ++b) {
+        if (b >= NS && !mbar_poll<0>(&sm->ax_empty[s], ((b / NS) & 1) ^ 1, abort_flag, a.status)) break;
+        mbar_arrive_expect_tx(&sm->full[s], C::kX);
+        bulk_load(sx + s * C::kX, src, C::kX, &sm->full[s], pol_x);
+        src += C::kX;
+        if (--left == 0) {   // the next tile: its tokens follow, or the first ones again
+          left = 2 * n_chunk;
+          if (++tt == a.tok_tiles) tt = 0, src = x;
+        }
+        if (++s == NS) s = 0;
+      }
+      if (*abort_flag)
+        for (int c = b > NS ? b - NS : 0; c < b; ++c) mbar_drain(&sm->full[c % NS], (c / NS) & 1);
+    }
+  } else if (warp <= 2) {
+    // ------------------------------ MMA issuers (whole warps, converged) ------------------------------
     constexpr uint32_t id = idesc_bf16_f32(128, BN, false, false);
     const uint64_t dX = sdesc_sw128(smem_u32(sx), 16, 1024);
+    const int me = warp - 1;
     bool ok = true;
-    uint32_t grp = 0;                            // groups begun so far
-    for (int b = 0; b < 2 * n_u; ++b) {
+    uint32_t n = 0;                              // groups begun by this warp
+    for (int b = me; b < 2 * n_u && ok; b += 2) {
       const int s = b % NS;
       ok = mbar_poll<0>(&sm->full[s], (b / NS) & 1, abort_flag, a.status);
       ok = __all_sync(0xffffffffu, ok);
@@ -157,31 +169,31 @@ __global__ void __launch_bounds__(W4TcCfg<BN>::kThreads, 1) w4_tc_kernel(const _
       const uint32_t ta = tA + s * C::kACols;
       const uint64_t dx = dX + s * (C::kX / 16);
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        if (kk % MPG == 0 && grp >= 2) {   // the buffer was read by the promoting warps
-          ok = ok && mbar_poll<0>(&sm->d_free[grp & 1], ((grp >> 1) & 1) ^ 1, abort_flag, a.status);
+      for (int g = 0; g < GPB; ++g, ++n) {
+        const int buf = me * C::kBufs + n % C::kBufs;
+        if (n >= C::kBufs) {   // the accumulator was read by the promoting warps
+          ok = mbar_poll<0>(&sm->d_free[buf], (n / C::kBufs & 1) ^ 1, abort_flag, a.status);
           ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           tc_fence_after();
         }
-        if (ok)
-          umma_bf16_ta_warp(tmem + (grp & 1) * BN, ta + kk * 8, dx + (kk >> 2) * (C::kX / 32) + (kk & 3) * 2, id,
-                            kk % MPG != 0 ? 1u : 0u);
-        if (kk % MPG == MPG - 1) {
-          if (ok) umma_commit_warp(&sm->d_full[grp & 1]);
-          ++grp;
+#pragma unroll
+        for (int k = 0; k < MPG; ++k) {
+          const int q = g * MPG + k;             // 16-k step of the block
+          umma_bf16_ta_warp(tmem + buf * BN, ta + q * 8, dx + (q >> 2) * (C::kX / 32) + (q & 3) * 2, id, k != 0 ? 1u : 0u);
         }
+        umma_commit_warp(&sm->d_full[buf]);
       }
-      if (!ok) break;
-      umma_commit_warp(&sm->ax_empty[s]);
+      if (ok) umma_commit_warp(&sm->ax_empty[s]);
     }
     if (!ok) {
-      umma_commit_warp(&sm->drain);
-      mbar_drain(&sm->drain, 0);
+      umma_commit_warp(&sm->drain[me]);
+      mbar_drain(&sm->drain[me], 0);
     }
-  } else if (warp < 2 + C::kEpi) {
+  } else if (warp < 4 + C::kEpi) {
     // ------------------------------ promotion ------------------------------
     const int q4 = warp & 3;
-    const int col0 = ((warp - 2) >> 2) * C::kCols;
+    const int col0 = ((warp - 4) >> 2) * C::kCols;
     const int row = q4 * 32 + lane;
     const uint32_t t_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16) + col0;
     constexpr int gpc = 16 / MPG;
@@ -191,22 +203,26 @@ __global__ void __launch_bounds__(W4TcCfg<BN>::kThreads, 1) w4_tc_kernel(const _
 #pragma unroll
     for (int j = 0; j < C::kCols; ++j) acc[j] = 0.f;
     const __nv_bfloat16* scales = static_cast<const __nv_bfloat16*>(a.scales);
-    // the scales of a chunk's groups (up to 8), one chunk ahead of their use
-    uint32_t next[4] = {0, 0, 0, 0};
-    auto load_scales = [&](int u) {
-      const int r = u / n_chunk / a.tok_tiles * 128 + row, first = (u % n_chunk) * gpc;
+    // the scales of a chunk's groups (up to 8), one chunk ahead of their use; at 64 columns a
+    // thread, where registers are short and groups slow, each one a group ahead
+    constexpr bool kOneScale = C::kCols == 64;
+    uint32_t next[kOneScale ? 1 : 4];
+    auto load_scales = [&](int rt, int ch) {
+      const int r = rt * 128 + row, first = ch * gpc;
       const __nv_bfloat16* p = scales + static_cast<int64_t>(r < a.N ? r : 0) * n_groups + first;
-      if (a.vec_scales) {
-        if (gpc == 8) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-          next[0] = v.x, next[1] = v.y, next[2] = v.z, next[3] = v.w;
-        } else if (gpc == 4) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-          next[0] = v.x, next[1] = v.y;
-        } else {
-          next[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      if constexpr (!kOneScale) {
+        if (a.vec_scales) {
+          if (gpc == 8) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+            next[0] = v.x, next[1] = v.y, next[2] = v.z, next[3] = v.w;
+          } else if (gpc == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+            next[0] = v.x, next[1] = v.y;
+          } else {
+            next[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          }
+          return;
         }
-      } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t lo = 2 * j < gpc && first + 2 * j < n_groups ? __bfloat16_as_ushort(p[2 * j]) : 0;
@@ -215,43 +231,70 @@ __global__ void __launch_bounds__(W4TcCfg<BN>::kThreads, 1) w4_tc_kernel(const _
         }
       }
     };
-    if (n_u > 0) load_scales(u_lo);
+    auto load_one = [&](int rt, int grp) {       // groups behind K scale nothing
+      const int r = rt * 128 + row;
+      next[0] = grp < n_groups
+                    ? __bfloat16_as_ushort(__ldg(scales + static_cast<int64_t>(r < a.N ? r : 0) * n_groups + grp))
+                    : 0;
+    };
+    int rt = rt0, tt = tt0, ch = ch0;      // of the current chunk
+    if (n_u > 0) {
+      load_scales(rt, ch);
+      if (kOneScale) load_one(rt, ch * gpc);
+    }
     uint32_t grp = 0;
     bool ok = true;
     int seg_lo = u_lo;   // first chunk of the current segment
     for (int u = u_lo; u < u_hi && ok; ++u) {
-      uint32_t cur[4] = {next[0], next[1], next[2], next[3]};
-      if (u + 1 < u_hi) load_scales(u + 1);
+      uint32_t cur[kOneScale ? 1 : 4];
+      if constexpr (!kOneScale) cur[0] = next[0], cur[1] = next[1], cur[2] = next[2], cur[3] = next[3];
+      const bool tile_end = ch + 1 == n_chunk;
+      const int rt_next = tile_end && tt + 1 == a.tok_tiles ? rt + 1 : rt;
+      if (u + 1 < u_hi) load_scales(rt_next, tile_end ? 0 : ch + 1);
 #pragma unroll 1
       for (int g = 0; g < gpc; ++g, ++grp) {
-        const uint32_t w = g < 4 ? (g < 2 ? cur[0] : cur[1]) : (g < 6 ? cur[2] : cur[3]);
-        const float s = __uint_as_float((g & 1) ? (w & 0xffff0000u) : (w << 16));
-        const uint32_t buf = grp & 1;
-        ok = mbar_poll<20>(&sm->d_full[buf], (grp >> 1) & 1, abort_flag, a.status);
+        float s;
+        if constexpr (kOneScale) {
+          s = __uint_as_float(next[0] << 16);
+          if (g + 1 < gpc)
+            load_one(rt, ch * gpc + g + 1);
+          else if (u + 1 < u_hi)
+            load_one(rt_next, tile_end ? 0 : (ch + 1) * gpc);
+        } else {
+          const uint32_t w = g < 4 ? (g < 2 ? cur[0] : cur[1]) : (g < 6 ? cur[2] : cur[3]);
+          s = __uint_as_float((g & 1) ? (w & 0xffff0000u) : (w << 16));
+        }
+        const uint32_t blk = grp / GPB, n = (blk >> 1) * GPB + grp % GPB;
+        const uint32_t buf = (blk & 1) * C::kBufs + n % C::kBufs;
+        ok = mbar_poll<20>(&sm->d_full[buf], n / C::kBufs & 1, abort_flag, a.status);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        constexpr int W = C::kCols == 32 ? 32 : 16;          // columns a wait (96 registers a thread at 64 columns)
 #pragma unroll
-        for (int c = 0; c < C::kCols; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(t_base + buf * BN + c, v);
+        for (int c = 0; c < C::kCols; c += W) {
+          uint32_t v[W / 16][16];
+#pragma unroll
+          for (int i = 0; i < W / 16; ++i) tmem_ld16(t_base + buf * BN + c + 16 * i, v[i]);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) acc[c + j] = fmaf(s, __uint_as_float(v[j]), acc[c + j]);
+          for (int j = 0; j < W; ++j) acc[c + j] = fmaf(s, __uint_as_float(v[j / 16][j % 16]), acc[c + j]);
         }
         tc_fence_before();
         mbar_arrive(&sm->d_free[buf]);
       }
       if (!ok) break;
-      const int tile = u / n_chunk;
-      if (u + 1 == u_hi || (u + 1) % n_chunk == 0) {   // segment end
-        const int r = tile / a.tok_tiles * 128 + row, t0 = tile % a.tok_tiles * BN + col0;
-        const bool whole = seg_lo == tile * n_chunk && u + 1 == (tile + 1) * n_chunk;
+      if (u + 1 == u_hi || tile_end) {   // segment end
+        const int r = rt * 128 + row, t0 = tt * BN + col0;
+        const bool whole = tile_end && u - seg_lo == ch;
         if (whole) {
-          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + r;
+          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + static_cast<int64_t>(t0) * a.N + r;
+          const int left = r < a.N ? a.T - t0 : 0;
 #pragma unroll
-          for (int j = 0; j < C::kCols; ++j)
-            if (r < a.N && t0 + j < a.T) y[static_cast<int64_t>(t0 + j) * a.N] = __float2bfloat16_rn(acc[j]);
+          for (int j = 0; j < C::kCols; ++j) {
+            if (j < left) *y = __float2bfloat16_rn(acc[j]);
+            y += a.N;
+          }
         } else {       // the CTA's first segment in slot 0, its last in slot 1
           float* p = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (seg_lo == u_lo ? 0 : 1)) * BN * 128 + row;
 #pragma unroll
@@ -261,12 +304,19 @@ __global__ void __launch_bounds__(W4TcCfg<BN>::kThreads, 1) w4_tc_kernel(const _
         for (int j = 0; j < C::kCols; ++j) acc[j] = 0.f;
         seg_lo = u + 1;
       }
+      if (tile_end) {
+        ch = 0;
+        if (++tt == a.tok_tiles) tt = 0, ++rt;
+      } else {
+        ++ch;
+      }
     }
   } else {
     // ------------------------------ expansion ------------------------------
-    const int wg = (warp - 2 - C::kEpi) >> 2;                    // half of a block
+    constexpr int kHalves = 8 / C::kExp;                         // 64-k halves of a block a thread expands
+    const int h0 = C::kExp == 8 ? (warp - 4 - C::kEpi) >> 2 : 0;
     const int row = (warp & 3) * 32 + lane;                      // a warp reaches the TMEM lanes of its quarter
-    const uint32_t t_dst = tA + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 32;
+    const uint32_t t_dst = tA + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t sw = row & 7;
     const uint32_t eight = 0x43084308u;                          // (136, 136)
     bool ok = true;
@@ -276,12 +326,15 @@ __global__ void __launch_bounds__(W4TcCfg<BN>::kThreads, 1) w4_tc_kernel(const _
       if (!ok) break;
       const uint8_t* src = codes + (i % NC) * C::kCode + row * 128;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = 2 * h + wg, b = 2 * i + h, s = b % NS;     // 64 k number j of the chunk, half wg of block b
-        uint4 w[2];
-        w[0] = *reinterpret_cast<const uint4*>(src + (((2 * j) ^ sw) << 4));
-        w[1] = *reinterpret_cast<const uint4*>(src + (((2 * j + 1) ^ sw) << 4));
-        if (h == 1) {   // this warp's codes of the chunk are in registers
+      for (int blk = 0; blk < 2; ++blk) {
+        const int b = 2 * i + blk, s = b % NS;
+        uint4 w[kHalves][2];
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            w[h][j] = *reinterpret_cast<const uint4*>(src + (((4 * blk + 2 * (h0 + h) + j) ^ sw) << 4));
+        if (blk == 1) {   // this warp's codes of the chunk are in registers
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm->code_empty[i % NC]);
         }
@@ -291,17 +344,19 @@ __global__ void __launch_bounds__(W4TcCfg<BN>::kThreads, 1) w4_tc_kernel(const _
           if (!ok) break;
         }
         tc_fence_after();
-        const uint32_t word[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-        for (int k = 0; k < 8; k += 4) {
-          uint32_t p[16];
+        for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            p[q] = w4_pair(word[k + (q >> 2)], q & 3);
-            asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(p[q]) : "r"(eight));
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t word[4] = {w[h][j].x, w[h][j].y, w[h][j].z, w[h][j].w};
+            uint32_t p[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              p[q] = w4_pair(word[q >> 2], q & 3);
+              asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(p[q]) : "r"(eight));
+            }
+            tmem_st16(t_dst + s * C::kACols + (h0 + h) * 32 + j * 16, p);
           }
-          tmem_st16(t_dst + s * C::kACols + k * 4, p);
-        }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sm->full[s]);
