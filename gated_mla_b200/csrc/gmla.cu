@@ -1019,16 +1019,17 @@ gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w, const v
 constexpr int kW4MaxK = 1 << 24;
 
 // workspace: status word, the activations in the order the kernel reads them, then their
-// group sums (few tokens) or the partial tiles (more)
-static size_t w4_act_bytes(const W4Plan& p) { return align256(static_cast<size_t>(p.T8) * p.K256 * 2); }
+// group sums among them (few tokens), then the partial tiles (more)
+static size_t w4_act_bytes(const W4Plan& p) {
+  return align256(static_cast<size_t>(p.T8) * p.K256 * 2 + static_cast<size_t>(p.T8) * p.n_chunk * 32);
+}
 
 size_t gmla_gate_out_w4_workspace_size(const gmla_config* cfg, int32_t T) {
   if (!cfg_valid(cfg) || T < 0) return 256;
   const size_t HD = static_cast<size_t>(cfg->n_heads) * cfg->d_h;
   if (T == 0 || HD > kW4MaxK) return 256;
   const W4Plan p = w4_plan(cfg->d_model, T, static_cast<int>(HD), num_sms());
-  return 256 + w4_act_bytes(p) +
-         (p.nt ? align256((HD / 32 + 1) * p.T8 * 4) : static_cast<size_t>(p.G) * 2 * p.bn * 128 * 4);
+  return 256 + w4_act_bytes(p) + static_cast<size_t>(p.G) * 2 * p.bn * 128 * 4;
 }
 
 gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const void* o, int32_t T,
@@ -1061,7 +1062,7 @@ gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const vo
   if (static_cast<int64_t>(plan.row_tiles) * plan.tok_tiles * plan.n_chunk > (int64_t(1) << 30))
     return fail(GMLA_ERR_UNSUPPORTED, "gate_out_w4: more than 2^30 tiles of work");
   float* rest = reinterpret_cast<float*>(act + w4_act_bytes(plan));
-  const W4PrepArgs p{o,        gate_logits,    act,            rest,      T,       K,          cfg->n_heads,
+  const W4PrepArgs p{o,        gate_logits,    act,            T,         K,       cfg->n_heads,
                      cfg->d_h, cfg->gate_mode, cfg->gate_topk, w4->group, plan.T8, plan.K256, plan.nt, plan.bn};
   cudaError_t e = launch_w4_prep(p, sms, st);
   if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4");
@@ -1073,7 +1074,6 @@ gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const vo
     W4Args a{};
     a.wmap = wmap;
     a.x = act;
-    a.sums = rest;
     a.scales = w4->scales;
     a.y = y;
     a.status = status;
@@ -1081,7 +1081,6 @@ gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const vo
     a.N = N;
     a.K = K;
     a.group = w4->group;
-    a.T8 = plan.T8;
     a.vec_scales = vec_scales;
     e = launch_w4_mma(a, plan, st);
   } else {

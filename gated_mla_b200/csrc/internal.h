@@ -238,19 +238,17 @@ constexpr int kW4Chunk = 256;   // k per pipeline stage
 struct W4PrepArgs {
   const void* o;             // [T, K] bf16
   const float* gate_logits;  // [T, G] or null
-  void* out;                 // [T8, K256] bf16 in the order the product reads
-  float* sums;               // [K / group, T8]: -136 sum of the group's activations
+  void* out;                 // in the order the product reads (w4.cu)
   int32_t T, K, H, d_h, gate_mode, gate_topk, group;
   int32_t T8, K256, nt, bn;  // of the plan
 };
 struct W4Args {
   CUtensorMap wmap;          // 2D [N, K / 2] bytes
   const void* x;             // w4_prep's out
-  const float* sums;
   const void* scales;        // [N, K / group] bf16
   void* y;                   // [T, N] bf16
   int* status;
-  int32_t T, N, K, group, T8;
+  int32_t T, N, K, group;
   int32_t vec_scales;        // the scales of a 256-k chunk are one aligned load
 };
 struct W4TcArgs {

@@ -34,7 +34,10 @@ namespace {
 
 constexpr int kW4Warps = 8;               // consumer warps; one more issues the copies
 constexpr int kW4Threads = 32 * (kW4Warps + 1);
-constexpr int kW4Rows = 16 * kW4Warps;    // weight rows per CTA
+// 16-row tiles a warp, which would share each activation fragment: two (and two CTAs an SM
+// instead of three) took 21.6 us against 21.8 at 7168 x 16384, but 8.2 against 6.9 at 4096 x 4096.
+constexpr int kW4Tiles = 1;
+constexpr int kW4Rows = 16 * kW4Tiles * kW4Warps;   // weight rows per CTA
 constexpr int kW4WBytes = kW4Rows * 128;  // codes of a stage: 128 bytes (256 k) a row
 
 __device__ __forceinline__ uint32_t w4_pair(uint32_t w, int i) {   // (128 + v_i, 128 + v_{i+4}) as bf16x2
@@ -45,7 +48,7 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t w, int i) {   // (128 + v_i
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -70,24 +73,23 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// CTAs that share an SM (by their shared memory and registers)
-constexpr int w4_ctas_per_sm(int nt) { return nt <= 2 ? 3 : (nt == 4 ? 2 : 1); }
+constexpr int kW4CtasPerSm = 3;           // by their shared memory
 
 struct W4Smem {
   uint64_t full[4], empty[4];
   int abort;
 };
 
-template <int NT>
 struct W4Cfg {
-  static constexpr int kXBytes = (kW4Chunk / 32) * NT * 512;   // [8 steps of 32 k][NT][32 lanes][16 bytes]
-  static constexpr int kStage = kW4WBytes + kXBytes;
+  static constexpr int kXFrag = (kW4Chunk / 32) * 512;         // [8 steps of 32 k][32 lanes][16 bytes]
+  static constexpr int kXBytes = kXFrag + 256;                 // then -136 sums [groups of the chunk, up to 8][8] fp32
+  static constexpr int kStage = (kW4WBytes + kXBytes + 1023) & ~1023;
   static constexpr int kStages = 3;
   static constexpr int kPitch = kW4Rows + 4;                   // floats between tokens of the partial tile
-  static constexpr int kRed = kPitch * 8 * NT * 4;             // fp32 partial tile, over the ring once it has drained
+  static constexpr int kRed = kPitch * 8 * 4;                  // fp32 partial tile, over the ring once it has drained
   static constexpr int kRing = kStage * kStages > kRed ? kStage * kStages : kRed;
   static constexpr int kSmem = kRing + 1024 + static_cast<int>(sizeof(W4Smem));
-  static constexpr int kCtas = w4_ctas_per_sm(NT);
+  static constexpr int kCtas = kW4CtasPerSm;
   static_assert(kStages <= 4, "barriers");
   static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory of the CTAs sharing an SM");
 };
@@ -102,10 +104,10 @@ namespace gmla {
 
 // ---------------------------------------------------------------------------
 // a = gate ⊙ o in bf16, in fragment order, and -136 times its sum over each group.
-// out: [T8 / 8nt blocks][K256 / 32 steps][nt][g * 4 + c][8 bf16]: token 8 n + g of the block,
-// k = 32 step + 8 c + (0 4 1 5 2 6 3 7); sums: [n_groups][T8] fp32. Tokens and k behind
-// the end are zeros. A thread makes one run of 8 k; the runs of a group are
-// neighbouring lanes. nt = 0 (for w4_tc): out is the image of the swizzled shared-memory
+// out: for each chunk of 256 k, [8 steps][g * 4 + c][8 bf16]: token g, k = 32 step + 8 c +
+// (0 4 1 5 2 6 3 7), then the sums [256 / group][8] fp32 in 256 bytes. Tokens and k behind
+// the end are zeros. A thread makes one run of 8 k; the runs of a group are neighbouring
+// lanes. nt = 0 (for w4_tc): out is the image of the swizzled shared-memory
 // tiles [T8 / bn][K256 / 64][bn][128 bytes], the runs of 8 in the same order, and no sums are made.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
@@ -114,7 +116,7 @@ __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
   const int k8 = a.K256 >> 3;
   const int64_t n = static_cast<int64_t>(a.T8) * k8;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  const int g8 = a.group >> 3, n_groups = a.K / a.group;
+  const int g8 = a.group >> 3;
   for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x; i0 < n; i0 += stride) {   // uniform over a block
     const int64_t i = i0 + threadIdx.x;
     const int t = static_cast<int>(i / k8);
@@ -160,22 +162,21 @@ __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
     for (int j = 0; j < 4; ++j) sum += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
     for (int o = 1; o < g8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (i < n) {
-      if (k < a.K && k % a.group == 0) a.sums[static_cast<int64_t>(k / a.group) * a.T8 + t] = -136.f * sum;
-      const int tb = t / (8 * a.nt), tn = t % (8 * a.nt);
-      const int64_t at = ((static_cast<int64_t>(tb) * (a.K256 >> 5) + (k >> 5)) * a.nt + (tn >> 3)) * 32 + (tn & 7) * 4 +
-                         ((k >> 3) & 3);
-      reinterpret_cast<uint4*>(a.out)[at] = r;
+      uint8_t* blk = static_cast<uint8_t*>(a.out) + static_cast<int64_t>(k / kW4Chunk) * W4Cfg::kXBytes;
+      if (k % a.group == 0)
+        reinterpret_cast<float*>(blk + W4Cfg::kXFrag)[k % kW4Chunk / a.group * 8 + t] = -136.f * sum;
+      reinterpret_cast<uint4*>(blk)[((k >> 5) & 7) * 32 + t * 4 + ((k >> 3) & 3)] = r;
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// few tokens. Grid (row tiles, tiles of 8 NT tokens, K splits); the splits of a
-// tile form a cluster. GPC groups per 256-k chunk (8, 4 or 2).
+// few tokens (up to 8). Grid (row tiles, 1, K splits); the splits of a tile form a cluster. GPC groups per 256-k chunk (8, 4 or 2).
 // ---------------------------------------------------------------------------
-template <int NT, int GPC>
-__global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(const __grid_constant__ W4Args a) {
-  using C = W4Cfg<NT>;
+template <int GPC>
+__global__ void __launch_bounds__(kW4Threads, W4Cfg::kCtas) w4_mma_kernel(const __grid_constant__ W4Args a) {
+  using C = W4Cfg;
+  constexpr int MT = kW4Tiles;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -184,8 +185,9 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = gridDim.z, rank = blockIdx.z;
   const int n_chunk = (a.K + kW4Chunk - 1) / kW4Chunk;
-  const int c_lo = n_chunk * rank / splits, c_hi = n_chunk * (rank + 1) / splits;
-  const int row0 = blockIdx.x * kW4Rows, t0 = blockIdx.y * 8 * NT;
+  // the splits take the chunks in turn, so that a cluster reads whole stretches of each row at a time
+  const int n_c = (n_chunk - rank + splits - 1) / splits;      // chunks rank, rank + splits, ..
+  const int row0 = blockIdx.x * kW4Rows;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(&sm->full[i], 1);
@@ -197,11 +199,11 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
   __syncthreads();
   if (threadIdx.x == 0) griddep_launch_dependents();
 
-  float acc[NT][4];
+  float acc[MT][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
+    for (int j = 0; j < 4; ++j) acc[m][j] = 0.f;
 
   int issued = 0;   // stages requested (copy thread)
   if (warp == kW4Warps) {
@@ -210,17 +212,16 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
       // this one before all earlier kernels are done, so they are requested before the wait
       tma_prefetch_desc(&a.wmap);
       const uint64_t pol_w = l2_evict_first(), pol_x = l2_evict_last();
-      const int n_c = c_hi - c_lo;
       const int pre = n_c < NS ? n_c : NS;
-      const uint8_t* x = static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(blockIdx.y) * n_chunk * C::kXBytes;
+      const uint8_t* x = static_cast<const uint8_t*>(a.x);
       auto load_w = [&](int i) {
         const int s = i % NS;
-        mbar_arrive_expect_tx(&sm->full[s], C::kStage);
-        tma_load_2d(&a.wmap, &sm->full[s], ring + s * C::kStage, (c_lo + i) * 128, row0, pol_w);
+        mbar_arrive_expect_tx(&sm->full[s], kW4WBytes + C::kXBytes);
+        tma_load_2d(&a.wmap, &sm->full[s], ring + s * C::kStage, (rank + i * splits) * 128, row0, pol_w);
       };
       auto load_x = [&](int i) {
         const int s = i % NS;
-        bulk_load(ring + s * C::kStage + kW4WBytes, x + static_cast<int64_t>(c_lo + i) * C::kXBytes, C::kXBytes,
+        bulk_load(ring + s * C::kStage + kW4WBytes, x + static_cast<int64_t>(rank + i * splits) * C::kXBytes, C::kXBytes,
                   &sm->full[s], pol_x);
       };
       for (int i = 0; i < pre; ++i) load_w(i);
@@ -236,53 +237,58 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
   } else {
     const int g = lane >> 2, c = lane & 3;
     const int n_groups = a.K / a.group;
-    const __nv_bfloat16* sc[2];
+    const __nv_bfloat16* sc[MT][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = row0 + warp * 16 + g + 8 * h;
-      sc[h] = static_cast<const __nv_bfloat16*>(a.scales) + static_cast<int64_t>(row < a.N ? row : 0) * n_groups;
-    }
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = row0 + (warp * MT + m) * 16 + g + 8 * h;
+        sc[m][h] = static_cast<const __nv_bfloat16*>(a.scales) + static_cast<int64_t>(row < a.N ? row : 0) * n_groups;
+      }
     // the scales of a chunk's groups, one chunk ahead of their use
-    uint32_t next[2][GPC / 2];
+    uint32_t next[MT][2][GPC / 2];
     auto load_scales = [&](int chunk) {
       const int first = chunk * GPC;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const __nv_bfloat16* p = sc[h] + first;
-        if (a.vec_scales) {
-          if constexpr (GPC == 8) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-            next[h][0] = v.x, next[h][1] = v.y, next[h][2] = v.z, next[h][3] = v.w;
-          } else if constexpr (GPC == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-            next[h][0] = v.x, next[h][1] = v.y;
-          } else {
-            next[h][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-          }
-        } else {
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int j = 0; j < GPC / 2; ++j) {   // groups behind K scale nothing (their activations are zeros)
-            const uint32_t lo = first + 2 * j < n_groups ? __bfloat16_as_ushort(p[2 * j]) : 0;
-            const uint32_t hi = first + 2 * j + 1 < n_groups ? __bfloat16_as_ushort(p[2 * j + 1]) : 0;
-            next[h][j] = lo | (hi << 16);
+        for (int h = 0; h < 2; ++h) {
+          const __nv_bfloat16* p = sc[m][h] + first;
+          uint32_t(&to)[GPC / 2] = next[m][h];
+          if (a.vec_scales) {
+            if constexpr (GPC == 8) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+              to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+            } else if constexpr (GPC == 4) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+              to[0] = v.x, to[1] = v.y;
+            } else {
+              to[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < GPC / 2; ++j) {   // groups behind K scale nothing (their activations are zeros)
+              const uint32_t lo = first + 2 * j < n_groups ? __bfloat16_as_ushort(p[2 * j]) : 0;
+              const uint32_t hi = first + 2 * j + 1 < n_groups ? __bfloat16_as_ushort(p[2 * j + 1]) : 0;
+              to[j] = lo | (hi << 16);
+            }
           }
         }
-      }
     };
-    if (c_lo < c_hi) load_scales(c_lo);
-    griddep_wait();   // the group sums come from w4_prep
-    const float* sums = a.sums + t0 + 2 * c;
-    // rows g and g + 8 of the warp's 16: word c of the 16-byte chunk j ^ g
-    const uint32_t w_off = (warp * 16 + g) * 128 + (g << 4) + 4 * c;
-    for (int ch = c_lo; ch < c_hi; ++ch) {
-      const int i = ch - c_lo, s = i % NS;
-      uint32_t cur[2][GPC / 2];
+    if (n_c > 0) load_scales(rank);
+    // rows g and g + 8 of a 16-row tile: word c of the 16-byte chunk j ^ g
+    const uint32_t w_off = (warp * MT * 16 + g) * 128 + (g << 4) + 4 * c;
+    for (int i = 0; i < n_c; ++i) {
+      const int s = i % NS;
+      uint32_t cur[MT][2][GPC / 2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int j = 0; j < GPC / 2; ++j) cur[h][j] = next[h][j];
-      if (ch + 1 < c_hi) load_scales(ch + 1);
-      bool ok = mbar_poll<0>(&sm->full[s], (i / NS) & 1, abort_flag, a.status);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < GPC / 2; ++j) cur[m][h][j] = next[m][h][j];
+      if (i + 1 < n_c) load_scales(rank + (i + 1) * splits);
+      bool ok = mbar_poll<20>(&sm->full[s], (i / NS) & 1, abort_flag, a.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint8_t* ws = ring + s * C::kStage;
@@ -290,44 +296,42 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
       constexpr int JPG = 8 / GPC;     // 32-k steps per group
 #pragma unroll
       for (int gr = 0; gr < GPC; ++gr) {
-        const int grp = ch * GPC + gr;
-        float2 corr[NT];
+        const float2 corr = *reinterpret_cast<const float2*>(ws + kW4WBytes + C::kXFrag + (gr * 8 + 2 * c) * 4);
+        // two chains of products: the latency of a warp's chain, not issue, sets its pace
+        float part[MT][4], part2[MT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          corr[n] = grp < n_groups ? __ldg(reinterpret_cast<const float2*>(sums + static_cast<int64_t>(grp) * a.T8 + n * 8))
-                                   : make_float2(0.f, 0.f);
-        float part[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) part[n][j] = 0.f;
+        for (int m = 0; m < MT; ++m) {
+          part[m][0] = corr.x, part[m][1] = corr.y, part[m][2] = corr.x, part[m][3] = corr.y;
+          part2[m][0] = part2[m][1] = part2[m][2] = part2[m][3] = 0.f;
+        }
 #pragma unroll
         for (int jj = 0; jj < JPG; ++jj) {
           const int j = gr * JPG + jj;         // 16 bytes of codes a row; lane c takes word c: k = 32 j + 8 c ..
-          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(ws + (w_off ^ (j << 4)));
-          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(ws + (w_off ^ (j << 4)) + 1024);
-          uint32_t f0[4], f1[4];
+          const uint4 x = *reinterpret_cast<const uint4*>(xs + j * 512);
+          const uint8_t* wp = ws + (w_off ^ (j << 4));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            f0[q] = w4_pair(w0, q);
-            f1[q] = w4_pair(w1, q);
-          }
+          for (int m = 0; m < MT; ++m) {
+            const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wp + m * 2048);
+            const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wp + m * 2048 + 1024);
+            uint32_t f0[4], f1[4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 x = *reinterpret_cast<const uint4*>(xs + (j * NT + n) * 512);
-            mma_16816(part[n], f0[0], f1[0], f0[1], f1[1], x.x, x.y);
-            mma_16816(part[n], f0[2], f1[2], f0[3], f1[3], x.z, x.w);
+            for (int q = 0; q < 4; ++q) {
+              f0[q] = w4_pair(w0, q);
+              f1[q] = w4_pair(w1, q);
+            }
+            mma_16816(part[m], f0[0], f1[0], f0[1], f1[1], x.x, x.y);
+            mma_16816(part2[m], f0[2], f1[2], f0[3], f1[3], x.z, x.w);
           }
         }
-        const uint32_t u0 = cur[0][gr >> 1], u1 = cur[1][gr >> 1];
-        const float s0 = __uint_as_float((gr & 1) ? (u0 & 0xffff0000u) : (u0 << 16));
-        const float s1 = __uint_as_float((gr & 1) ? (u1 & 0xffff0000u) : (u1 << 16));
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[n][0] = fmaf(part[n][0] + corr[n].x, s0, acc[n][0]);
-          acc[n][1] = fmaf(part[n][1] + corr[n].y, s0, acc[n][1]);
-          acc[n][2] = fmaf(part[n][2] + corr[n].x, s1, acc[n][2]);
-          acc[n][3] = fmaf(part[n][3] + corr[n].y, s1, acc[n][3]);
+        for (int m = 0; m < MT; ++m) {
+          const uint32_t u0 = cur[m][0][gr >> 1], u1 = cur[m][1][gr >> 1];
+          const float s0 = __uint_as_float((gr & 1) ? (u0 & 0xffff0000u) : (u0 << 16));
+          const float s1 = __uint_as_float((gr & 1) ? (u1 & 0xffff0000u) : (u1 << 16));
+          acc[m][0] = fmaf(part[m][0] + part2[m][0], s0, acc[m][0]);
+          acc[m][1] = fmaf(part[m][1] + part2[m][1], s0, acc[m][1]);
+          acc[m][2] = fmaf(part[m][2] + part2[m][2], s1, acc[m][2]);
+          acc[m][3] = fmaf(part[m][3] + part2[m][3], s1, acc[m][3]);
         }
       }
       __syncwarp();
@@ -341,24 +345,24 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
     __syncthreads();
   }
   griddep_wait();   // y may still be read by an earlier kernel
-  // every copy has landed and been read: the ring becomes the partial tile [8 NT tokens][rows]
+  // every copy has landed and been read: the ring becomes the partial tile [8 tokens][rows]
   float* red = reinterpret_cast<float*>(ring);
   if (warp < kW4Warps) {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) red[(n * 8 + 2 * c + (j & 1)) * C::kPitch + warp * 16 + g + 8 * (j >> 1)] = acc[n][j];
+      for (int j = 0; j < 4; ++j)
+        red[(2 * c + (j & 1)) * C::kPitch + (warp * MT + m) * 16 + g + 8 * (j >> 1)] = acc[m][j];
   }
   if (splits > 1)
     cluster_sync_all();
   else
     __syncthreads();
   // CTA `rank` adds up its share of the tile's rows, four at a time, over the splits in order
-  const int tokens = min(8 * NT, a.T - t0);
   const int q_lo = (kW4Rows / 4) * rank / splits, q_n = (kW4Rows / 4) * (rank + 1) / splits - q_lo;
   const uint32_t red_addr = smem_u32(red);
-  for (int i = threadIdx.x; i < tokens * q_n; i += kW4Threads) {
+  for (int i = threadIdx.x; i < a.T * q_n; i += kW4Threads) {
     const int t = i / q_n, r = (q_lo + i % q_n) * 4;
     if (row0 + r >= a.N) continue;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -373,7 +377,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
     } else {
       v = *reinterpret_cast<const float4*>(red + t * C::kPitch + r);
     }
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + static_cast<int64_t>(t0 + t) * a.N + row0 + r;
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + static_cast<int64_t>(t) * a.N + row0 + r;
     if (a.N % 4 == 0) {
       *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     } else {
@@ -389,42 +393,32 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <int NT, int GPC>
+template <int GPC>
 static cudaError_t launch_w4(const W4Args& a, int splits, cudaStream_t st) {
-  using C = W4Cfg<NT>;
-  auto k = w4_mma_kernel<NT, GPC>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  auto k = w4_mma_kernel<GPC>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, W4Cfg::kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.N + kW4Rows - 1) / kW4Rows, (a.T + 8 * NT - 1) / (8 * NT), splits);
+  const dim3 grid((a.N + kW4Rows - 1) / kW4Rows, 1, splits);
   prof_begin(st, "w4_mma");
-  e = launch_pdl(k, grid, dim3(kW4Threads), C::kSmem, st, splits, a);
+  e = launch_pdl(k, grid, dim3(kW4Threads), W4Cfg::kSmem, st, splits, a);
   prof_end(st);
   return e;
 }
 
-template <int NT>
-static cudaError_t launch_w4_group(const W4Args& a, int splits, cudaStream_t st) {
-  switch (a.group) {
-    case 32: return launch_w4<NT, 8>(a, splits, st);
-    case 64: return launch_w4<NT, 4>(a, splits, st);
-    default: return launch_w4<NT, 2>(a, splits, st);
-  }
-}
-
-// Up to kW4MaxMma tokens on m16n8k16 (measured against w4_tc at d_model 7168, K 16384:
-// see below), more on tcgen05.
+// Up to kW4MaxMma tokens on m16n8k16, more on tcgen05 (at 7168 x 16384, 8 tokens: 22.5 us
+// against 28.0).
 //
-// m16n8k16: token tile 8 or 16. K splits: the number (1 .. 8, one cluster) with the least
-// time, counted as waves of resident CTAs times the chunks that each works through
-// plus about two chunks' time for its start and its sum.
+// m16n8k16: K splits: the number (1 .. 8, one cluster) with the least time, counted as
+// waves of resident CTAs times the chunks that each works through plus about two chunks'
+// time for its start and its sum.
 // tcgen05: token tile the smallest of 16 .. 128 that holds T; one CTA per SM.
 W4Plan w4_plan(int N, int T, int K, int num_sms) {
   W4Plan p{};
   const int chunks = (K + kW4Chunk - 1) / kW4Chunk;
-  const int64_t row_tiles = (N + kW4Rows - 1) / kW4Rows;
   p.n_chunk = chunks;
-  p.row_tiles = static_cast<int>(row_tiles);
   if (T > kW4MaxMma) {
+    const int64_t row_tiles = (N + 127) / 128;
+    p.row_tiles = static_cast<int>(row_tiles);
     p.bn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
     p.tok_tiles = (T + p.bn - 1) / p.bn;
     const int64_t U = row_tiles * p.tok_tiles * chunks;
@@ -433,17 +427,17 @@ W4Plan w4_plan(int N, int T, int K, int num_sms) {
     p.K256 = chunks * kW4Chunk;
     return p;
   }
-  p.nt = T <= 8 ? 1 : 2;
-  p.tok_tiles = (T + 8 * p.nt - 1) / (8 * p.nt);
-  const int64_t tiles = row_tiles * p.tok_tiles;
-  const int64_t slots = static_cast<int64_t>(num_sms) * w4_ctas_per_sm(p.nt);
+  p.nt = 1;
+  p.tok_tiles = 1;
+  p.row_tiles = (N + kW4Rows - 1) / kW4Rows;
+  const int64_t slots = static_cast<int64_t>(num_sms) * kW4CtasPerSm;
   int64_t best = 0;
   for (int s = 1; s <= 8 && s <= chunks; ++s) {
-    const int64_t cost = ((tiles * s + slots - 1) / slots) * ((chunks + s - 1) / s + 2);
+    const int64_t cost = ((static_cast<int64_t>(p.row_tiles) * s + slots - 1) / slots) * ((chunks + s - 1) / s + 2);
     if (s == 1 || cost < best) best = cost, p.splits = s;
   }
   p.K256 = chunks * kW4Chunk;
-  p.T8 = p.tok_tiles * 8 * p.nt;
+  p.T8 = 8;
   return p;
 }
 
@@ -458,7 +452,11 @@ cudaError_t launch_w4_prep(const W4PrepArgs& a, int num_sms, cudaStream_t st) {
 }
 
 cudaError_t launch_w4_mma(const W4Args& a, const W4Plan& p, cudaStream_t st) {
-  return p.nt == 1 ? launch_w4_group<1>(a, p.splits, st) : launch_w4_group<2>(a, p.splits, st);
+  switch (a.group) {
+    case 32: return launch_w4<8>(a, p.splits, st);
+    case 64: return launch_w4<4>(a, p.splits, st);
+    default: return launch_w4<2>(a, p.splits, st);
+  }
 }
 
 template <int BN, int MPG>
