@@ -74,7 +74,8 @@ __device__ __forceinline__ void store8(float* p, int n, bool vec, const float (&
 
 // One row per `warps` warps; VPT vectors of 8 elements a thread (vector i of lane t
 // covers elements 8 (i * 32 * warps + t) ..). blockDim = warps * 32 * rows a block.
-template <typename T, int VPT>
+// VEC: d and the row strides allow 16-byte accesses, and every vector is whole.
+template <typename T, int VPT, bool VEC, bool GRP>
 __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a) {
   __shared__ float s_sum[32];
   griddep_wait();
@@ -84,50 +85,64 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a) {
   const int warp0 = threadIdx.x / tpr * a.warps;      // first warp of this row in the block
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
   const bool live = row < a.T;
-  const bool vec = a.vec != 0;
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   const T* r = static_cast<const T*>(a.residual) + row * a.residual_stride;
   T* ro = static_cast<T*>(a.residual_out) + row * a.residual_out_stride;
   T* out = static_cast<T*>(a.out) + row * a.out_stride;
-  float v[VPT][8];
-  float sum = 0.f;
+  const T* wt = static_cast<const T*>(a.weight);
+  float v[VPT][8], w8[VPT][8];
+  // every load of the row, then the weights (held for after the reduction)
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int e = (i * tpr + lane_r) * 8;
     const int n = live ? min(8, a.d - e) : 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    if (n > 0) {
-      load8<T>(x + e, n, vec, v[i]);
-      if (a.residual) {
-        float u[8];
-        load8<T>(r + e, n, vec, u);
+    if (n > 0) load8<T>(x + e, n, VEC, v[i]);
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int e = (i * tpr + lane_r) * 8;
+      const int n = live ? min(8, a.d - e) : 0;
+      float u[8];
+      if (n > 0) {
+        load8<T>(r + e, n, VEC, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] += u[j];
       }
     }
   }
+  if (VPT <= 2 && wt) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int e = (i * tpr + lane_r) * 8;
+      const int n = live ? min(8, a.d - e) : 0;
+      if (n > 0) load8<T>(wt + e, n, VEC, w8[i]);
+    }
+  }
+  float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int e = (i * tpr + lane_r) * 8;
     const int n = live ? min(8, a.d - e) : 0;
-    if (n > 0 && a.residual_out) store8(ro + e, n, vec, v[i]);
+    if (n > 0 && a.residual_out) store8(ro + e, n, VEC, v[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (a.warps > 1) {
-    const int w = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) s_sum[w] = sum;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) s_sum[threadIdx.x >> 5] = sum;
     __syncthreads();
-    sum = 0.f;
-    for (int i = 0; i < a.warps; ++i) sum += s_sum[warp0 + i];
+    sum = lane < a.warps ? s_sum[warp0 + lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
   const float inv = rsqrtf(sum / static_cast<float>(a.d) + a.eps);
-  const T* wt = static_cast<const T*>(a.weight);
   const int g8 = a.group >> 3;           // lanes a group spans
-  const int n_group = a.group ? (a.d + a.group - 1) / a.group : 0;
+  const int n_group = GRP ? (a.d + a.group - 1) / a.group : 0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int e = (i * tpr + lane_r) * 8;
@@ -136,36 +151,41 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = v[i][j] * inv;
     if (n > 0 && wt) {
-      float w8[8];
-      load8<T>(wt + e, n, vec, w8);
+      if (VPT > 2) load8<T>(wt + e, n, VEC, w8[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] *= w8[j];
+      for (int j = 0; j < 8; ++j) y[j] *= w8[i][j];
     }
-    if (n > 0 && a.out) store8(out + e, n, vec, y);
-    if (a.group) {
+    if (n > 0 && a.out) store8(out + e, n, VEC, y);
+    if (GRP) {
       float top = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, j < n ? fabsf(y[j]) : 0.f);
-      for (int o = 1; o < g8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, VEC || j < n ? fabsf(y[j]) : 0.f);
+      if (n <= 0) top = 0.f;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1)
+        if (o < g8) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       if (n > 0) {
-        const float part = top / 448.f;              // 0 for a group of zeros (or of values too small to divide)
+        const float part = top * (1.f / 448.f);      // 0 for a group of zeros (or of values too small to scale)
         const float scale = part > 0.f ? part : 1.f;
         const float mul = 1.f / scale;
         if ((threadIdx.x & (g8 - 1)) == 0) a.scales[row * n_group + e / a.group] = scale;
         uint8_t* c = a.codes + row * a.d + e;
         // a scale below fp32's normal range has no finite reciprocal: divide there
-        const bool div = !(mul < 3.0e38f);
+        if (!(mul < 3.0e38f)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = y[j] / scale;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] *= mul;
+        }
         uint32_t w[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float q[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) q[j] = div ? y[4 * h + j] / scale : y[4 * h + j] * mul;
-          w[h] = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3) |
-                 (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3))
+        for (int h = 0; h < 2; ++h)
+          w[h] = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * h], y[4 * h + 1]), __NV_SATFINITE, __NV_E4M3) |
+                 (static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(y[4 * h + 2], y[4 * h + 3]),
+                                                                 __NV_SATFINITE, __NV_E4M3))
                   << 16);
-        }
-        if (vec) {
+        if (VEC) {
           *reinterpret_cast<uint2*>(c) = make_uint2(w[0], w[1]);
         } else {
 #pragma unroll
@@ -177,13 +197,19 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a) {
   }
 }
 
-template <typename T>
+template <typename T, bool VEC, bool GRP>
 static cudaError_t launch_norm(const NormArgs& a, int vpt, dim3 grid, dim3 block, cudaStream_t st) {
   switch (vpt) {
-    case 1: return launch_pdl(add_rms_norm_kernel<T, 1>, grid, block, 0, st, 1, a);
-    case 2: return launch_pdl(add_rms_norm_kernel<T, 2>, grid, block, 0, st, 1, a);
-    default: return launch_pdl(add_rms_norm_kernel<T, 4>, grid, block, 0, st, 1, a);
+    case 1: return launch_pdl(add_rms_norm_kernel<T, 1, VEC, GRP>, grid, block, 0, st, 1, a);
+    case 2: return launch_pdl(add_rms_norm_kernel<T, 2, VEC, GRP>, grid, block, 0, st, 1, a);
+    default: return launch_pdl(add_rms_norm_kernel<T, 4, VEC, GRP>, grid, block, 0, st, 1, a);
   }
+}
+
+template <typename T>
+static cudaError_t launch_norm_t(const NormArgs& a, int vpt, dim3 grid, dim3 block, cudaStream_t st) {
+  if (a.vec) return a.group ? launch_norm<T, true, true>(a, vpt, grid, block, st) : launch_norm<T, true, false>(a, vpt, grid, block, st);
+  return a.group ? launch_norm<T, false, true>(a, vpt, grid, block, st) : launch_norm<T, false, false>(a, vpt, grid, block, st);
 }
 
 cudaError_t launch_add_rms_norm(NormArgs a, bool f32, int num_sms, cudaStream_t st) {
@@ -194,20 +220,19 @@ cudaError_t launch_add_rms_norm(NormArgs a, bool f32, int num_sms, cudaStream_t 
   const dim3 block(a.warps * 32 * rows);
   const dim3 grid((a.T + rows - 1) / rows);
   prof_begin(st, "add_rms_norm");
-  cudaError_t e = f32 ? launch_norm<float>(a, vpt, grid, block, st) : launch_norm<__nv_bfloat16>(a, vpt, grid, block, st);
+  cudaError_t e = f32 ? launch_norm_t<float>(a, vpt, grid, block, st) : launch_norm_t<__nv_bfloat16>(a, vpt, grid, block, st);
   prof_end(st);
   return e;
 }
 
-// Vectors a thread: 1 where the rows are few (the shortest chain: every element's
-// load is in flight at once), more where they are many, so that a block is small
-// and an SM holds several rows in different phases.
+// Vectors a thread. Few rows: as few as 32 warps allow (the shortest chain: 8 rows of 7168
+// take 2.6 us with one, 3.8 with four). Many: about 8 warps a row, so that an SM holds
+// several rows in different phases (16384 rows of 7168: 176 us with four, 0.82 of the HBM
+// rate, 210 with two, 191 with one; of 2048: 51, 56 and 47).
 int norm_vectors(int d, int T, int num_sms) {
   const int nvec = (d + 7) / 8;
-  if (nvec > 2048) return 4;
-  if (nvec > 1024) return 2;
-  if (T <= 2 * num_sms) return 1;
-  return nvec > 256 ? 4 : (nvec > 64 ? 2 : 1);
+  if (T <= 2 * num_sms) return nvec <= 1024 ? 1 : (nvec <= 2048 ? 2 : 4);
+  return nvec <= 256 ? 1 : (nvec <= 512 ? 2 : 4);
 }
 
 }  // namespace gmla
