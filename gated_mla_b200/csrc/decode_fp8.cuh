@@ -202,6 +202,12 @@ struct Dec8Smem {
 // the 256 columns of tensor memory it needs), so one CTA's loads, softmax and
 // MMAs overlap the other's; each CTA on its own is bound by the latency of
 // that chain, not by bandwidth. 32 heads: one CTA per SM with a deeper ring.
+// Waits of the producer and the softmax warps.
+template <bool BLK>
+__device__ __forceinline__ bool wait8(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  return BLK ? mbar_poll<20>(bar, parity, abort, status) : mbar_wait(bar, parity, abort, status);
+}
+
 template <int HG, bool BLK>
 struct Dec8Cfg {
   static constexpr int kN2 = 2 * HG;                         // hi and lo columns of the scores
@@ -293,7 +299,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
       const int L = sg.w;
       if (seg_heads(a, b, hg, heads_valid) == 0) continue;
       if (lane == 0) {
-        if (nq > 0 && !mbar_wait(&sm->q_empty, (nq - 1) & 1, abort_flag, a.status)) ok = false;
+        if (nq > 0 && !wait8<BLK>(&sm->q_empty, (nq - 1) & 1, abort_flag, a.status)) ok = false;
         if (ok) {
           mbar_arrive_expect_tx(&sm->q_full, C::kQBytes);
           for (int j = 0; j < kNB8; ++j)
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
           const uint32_t slot = nbox % NR;
           if (lane == 0) {
             if (nbox >= static_cast<uint32_t>(NR) &&
-                !mbar_wait(&sm->empty[slot], ((nbox / NR) & 1) ^ 1, abort_flag, a.status))
+                !wait8<BLK>(&sm->empty[slot], ((nbox / NR) & 1) ^ 1, abort_flag, a.status))
               ok = false;
             if (ok) mbar_arrive_expect_tx(&sm->full[slot], tx);
           }
@@ -340,7 +346,76 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
     }
   } else if (warp == 1) {
     // ------------------------------ MMA issuer ------------------------------
-    if (lane == 0) {
+    if constexpr (BLK) {   // the whole warp, converged (see umma_f8_warp)
+      constexpr uint32_t idS = idesc_e4m3_f32(128, N2, false, false);
+      constexpr uint32_t idO = idesc_e4m3_f32(128, NP, true, false);
+      const uint32_t ring_a = smem_u32(ring);
+      const uint64_t dRing = sdesc_sw128(ring_a, 16, 1024), dQ = sdesc_sw128(smem_u32(qs), 16, 1024);
+      const uint64_t dRingMN = sdesc_sw128(ring_a, kBox8, 1024);   // a box read as [tokens (K) x 128 latent dims (M)]
+      const uint64_t dP = sdesc_sw128(smem_u32(pbuf), 16, 1024);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_poll<0>(bar, parity, abort_flag, a.status)) != 0;
+      };
+      auto s_box = [&](uint32_t slot, int j, uint32_t tSb) {   // S^T += box j of the tile x its Q box
+        const uint64_t da = dRing + slot * (kBox8 / 16);
+        const uint64_t db = dQ + j * (N2 * 128 / 16);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma_f8_warp(tSb, da + kk * 2, db + kk * 2, idS, (j | kk) != 0);
+      };
+      uint32_t nbox = 0, ntile = 0, nseg = 0;
+      int early = 0;
+      bool ok = true;
+      if (a.test_stall && g == 0 && hg == 0) ok = wait(&sm->never, 0);
+      for (int si = seg_lo; si < seg_hi && ok; ++si) {
+        const int4 sg = a.seg_info[si];
+        if (seg_heads(a, sg.x, hg, heads_valid) == 0) continue;
+        ok = wait(&sm->q_full, nseg & 1);
+        for (int t = sg.y; t < sg.z && ok; ++t, ++ntile) {
+          const uint32_t tSb = tmem + (ntile & 1) * N2;
+          for (int j = early; j < kNB8 && ok; ++j) {
+            const uint32_t c = nbox + j;
+            ok = wait(&sm->full[c % NR], (c / NR) & 1);
+            if (ok) s_box(c % NR, j, tSb);
+          }
+          if (!ok) break;
+          if (t + 1 == sg.z) umma_commit_warp(&sm->q_empty);
+          umma_commit_warp(&sm->s_full);
+          // the next tile's boxes that have landed (a non-blocking probe)
+          early = 0;
+          if (t + 1 < sg.z) {
+            const uint32_t tSn = tmem + ((ntile + 1) & 1) * N2;
+            for (int j = 0; j < kNB8; ++j) {
+              const uint32_t c = nbox + kNB8 + j;
+              if (!__all_sync(0xffffffffu, mbar_test(&sm->full[c % NR], (c / NR) & 1))) break;
+              s_box(c % NR, j, tSn);
+              ++early;
+            }
+          }
+          ok = wait(&sm->p_full, ntile & 1);
+          const bool first = (t == sg.y);
+          if (ok && first && nseg > 0) ok = wait(&sm->o_free, (nseg - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int j = 0; j < kNB8; ++j) {
+            const uint32_t slot = (nbox + j) % NR;
+            const uint64_t da = dRingMN + slot * (kBox8 / 16);
+#pragma unroll
+            for (int kk = 0; kk < kTok / 32; ++kk)
+              umma_f8_warp(tO + j * NP, da + kk * (4096 / 16), dP + kk * 2, idO, (!first || kk > 0) ? 1u : 0u);
+            umma_commit_warp(&sm->empty[slot]);
+          }
+          nbox += kNB8;
+        }
+        if (!ok) break;
+        umma_commit_warp(&sm->o_done);
+        ++nseg;
+      }
+      if (!ok) {
+        umma_commit_warp(&sm->drain);
+        mbar_drain(&sm->drain, 0);
+      }
+    } else if (lane == 0) {
       constexpr uint32_t idS = idesc_e4m3_f32(128, N2, false, false);
       constexpr uint32_t idO = idesc_e4m3_f32(128, NP, true, false);
       const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(qs), p_a = smem_u32(pbuf);
@@ -476,7 +551,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
           lg = __log2f(sc);
           isc = 1.f / sc;
         }
-        ok = ok && mbar_wait(&sm->s_full, ntile & 1, abort_flag, a.status);
+        ok = ok && wait8<BLK>(&sm->s_full, ntile & 1, abort_flag, a.status);
         tc_fence_after();
         const uint32_t tS = tmem + (ntile & 1) * N2 + lane_off + h0;
         const int valid = min(kTok, L - t * kTok);
@@ -603,7 +678,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
         nbox += kNB8;
       }
       // ---- segment end: the partial (O, m, l)
-      ok = ok && mbar_wait(&sm->o_done, nseg & 1, abort_flag, a.status);
+      ok = ok && wait8<BLK>(&sm->o_done, nseg & 1, abort_flag, a.status);
       tc_fence_after();
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
