@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(256) decode_absorb_fp8_kernel(DecodeArgs a) {
 // ---------------------------------------------------------------------------
 struct Dec8Smem {
   uint64_t full[16], empty[16];   // per ring box
-  uint64_t q_full, q_empty, s_full, p_full, o_done, o_free, drain, never;
+  uint64_t s_full[2];             // by tile where scores run a tile ahead (kPipe), else the first
+  uint64_t q_full, q_empty, p_full, pv_done, o_done, o_free, drain, never;
   uint32_t tmem;
   int abort;
   int vote[3];
@@ -217,7 +218,13 @@ struct Dec8Cfg {
   static constexpr int kThreads = 64 + 128 * kSG;
   static constexpr int kCtasPerSm = HG == 16 ? 2 : 1;
   static constexpr int kQBytes = kNB8 * kN2 * 128;           // 4 boxes of [2 HG rows x 128 B]
-  static constexpr int kPBytes = ((kNP * 128) + 1023) & ~1023;   // [terms x HG rows x 128 tokens]
+  // Two P buffers where the ring holds two tiles (32 heads, block scales): the scores of
+  // a tile are complete, and its softmax runs, while the weighted sum of the tile before is
+  // still being taken. (With one buffer a tile's softmax and weighted sum took turns:
+  // 575 us for 8 x 131072 tokens and 128 heads.)
+  static constexpr bool kPipe = BLK && HG == 32;
+  static constexpr int kPBuf = ((kNP * 128) + 1023) & ~1023;     // [terms x HG rows x 128 tokens]
+  static constexpr int kPBytes = (kPipe ? 2 : 1) * kPBuf;
   static constexpr int kStruct = (static_cast<int>(sizeof(Dec8Smem)) + 127) & ~127;
   static constexpr int kFixed = kQBytes + kPBytes + kStruct + 1024 /*align*/;
   // shared memory of an SM (233472 B) less 1 KB reserved per CTA
@@ -229,7 +236,7 @@ struct Dec8Cfg {
   // the next tile's boxes are probed by the parity of their full barrier, which
   // is unambiguous while box c - kRing has been waited for: true up to c =
   // (first box of this tile) + 2 kNB8 - 1 when kRing >= kNB8
-  static_assert(kRing >= kNB8 + 1, "the ring holds more than one tile");
+  static_assert(kRing >= (kPipe ? 2 * kNB8 : kNB8 + 1), "the ring holds more than one tile, or two");
   static_assert(2 * kN2 + 4 * kNP <= kTmemCols, "scores and sums fit tensor memory");
   static_assert(kCtasPerSm * kTmemCols <= 512, "tensor memory of the CTAs sharing an SM");
 };
@@ -257,8 +264,10 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
     }
     mbar_init(&sm->q_full, 1);
     mbar_init(&sm->q_empty, 1);
-    mbar_init(&sm->s_full, 1);
+    mbar_init(&sm->s_full[0], 1);
+    mbar_init(&sm->s_full[1], 1);
     mbar_init(&sm->p_full, 128 * C::kSG);
+    mbar_init(&sm->pv_done, 1);
     mbar_init(&sm->o_done, 1);
     mbar_init(&sm->o_free, 128 * C::kSG);
     mbar_init(&sm->drain, 1);
@@ -370,41 +379,63 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
         const int4 sg = a.seg_info[si];
         if (seg_heads(a, sg.x, hg, heads_valid) == 0) continue;
         ok = wait(&sm->q_full, nseg & 1);
-        for (int t = sg.y; t < sg.z && ok; ++t, ++ntile) {
-          const uint32_t tSb = tmem + (ntile & 1) * N2;
-          for (int j = early; j < kNB8 && ok; ++j) {
-            const uint32_t c = nbox + j;
+        // scores of the tile whose first box is number c0, into buffer buf
+        auto scores = [&](uint32_t c0, int from, uint32_t buf) {
+          for (int j = from; j < kNB8 && ok; ++j) {
+            const uint32_t c = c0 + j;
             ok = wait(&sm->full[c % NR], (c / NR) & 1);
-            if (ok) s_box(c % NR, j, tSb);
+            if (ok) s_box(c % NR, j, tmem + buf * N2);
           }
-          if (!ok) break;
-          if (t + 1 == sg.z) umma_commit_warp(&sm->q_empty);
-          umma_commit_warp(&sm->s_full);
-          // the next tile's boxes that have landed (a non-blocking probe)
-          early = 0;
-          if (t + 1 < sg.z) {
-            const uint32_t tSn = tmem + ((ntile + 1) & 1) * N2;
-            for (int j = 0; j < kNB8; ++j) {
-              const uint32_t c = nbox + kNB8 + j;
-              if (!__all_sync(0xffffffffu, mbar_test(&sm->full[c % NR], (c / NR) & 1))) break;
-              s_box(c % NR, j, tSn);
-              ++early;
-            }
-          }
-          ok = wait(&sm->p_full, ntile & 1);
-          const bool first = (t == sg.y);
-          if (ok && first && nseg > 0) ok = wait(&sm->o_free, (nseg - 1) & 1);
-          if (!ok) break;
+        };
+        auto weighted_sum = [&](bool first) {
           tc_fence_after();
+          const uint64_t dPb = dP + (C::kPipe ? (ntile & 1) * (C::kPBuf / 16) : 0);
 #pragma unroll 1
           for (int j = 0; j < kNB8; ++j) {
             const uint32_t slot = (nbox + j) % NR;
             const uint64_t da = dRingMN + slot * (kBox8 / 16);
 #pragma unroll
             for (int kk = 0; kk < kTok / 32; ++kk)
-              umma_f8_warp(tO + j * NP, da + kk * (4096 / 16), dP + kk * 2, idO, (!first || kk > 0) ? 1u : 0u);
+              umma_f8_warp(tO + j * NP, da + kk * (4096 / 16), dPb + kk * 2, idO, (!first || kk > 0) ? 1u : 0u);
             umma_commit_warp(&sm->empty[slot]);
           }
+        };
+        if (C::kPipe && ok) {
+          scores(nbox, 0, ntile & 1);
+          if (ok && sg.y + 1 == sg.z) umma_commit_warp(&sm->q_empty);
+          if (ok) umma_commit_warp(&sm->s_full[ntile & 1]);
+        }
+        for (int t = sg.y; t < sg.z && ok; ++t, ++ntile) {
+          const bool last = t + 1 == sg.z;
+          if (C::kPipe) {   // the next tile's scores go before this tile's weighted sum
+            if (!last) {
+              scores(nbox + kNB8, 0, (ntile + 1) & 1);
+              if (!ok) break;
+              if (t + 2 == sg.z) umma_commit_warp(&sm->q_empty);
+              umma_commit_warp(&sm->s_full[(ntile + 1) & 1]);
+            }
+          } else {
+            scores(nbox, early, ntile & 1);
+            if (!ok) break;
+            if (last) umma_commit_warp(&sm->q_empty);
+            umma_commit_warp(&sm->s_full[0]);
+            // the next tile's boxes that have landed (a non-blocking probe)
+            early = 0;
+            if (!last) {
+              for (int j = 0; j < kNB8; ++j) {
+                const uint32_t c = nbox + kNB8 + j;
+                if (!__all_sync(0xffffffffu, mbar_test(&sm->full[c % NR], (c / NR) & 1))) break;
+                s_box(c % NR, j, tmem + ((ntile + 1) & 1) * N2);
+                ++early;
+              }
+            }
+          }
+          ok = wait(&sm->p_full, ntile & 1);
+          const bool first = (t == sg.y);
+          if (ok && first && nseg > 0) ok = wait(&sm->o_free, (nseg - 1) & 1);
+          if (!ok) break;
+          weighted_sum(first);
+          if (C::kPipe) umma_commit_warp(&sm->pv_done);
           nbox += kNB8;
         }
         if (!ok) break;
@@ -445,7 +476,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
           }
           if (!ok) break;
           if (t + 1 == sg.z) umma_commit(&sm->q_empty);
-          umma_commit(&sm->s_full);
+          umma_commit(&sm->s_full[0]);
           // the next tile's boxes that have landed (a non-blocking probe)
           early = 0;
           if (t + 1 < sg.z) {
@@ -551,7 +582,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
           lg = __log2f(sc);
           isc = 1.f / sc;
         }
-        ok = ok && wait8<BLK>(&sm->s_full, ntile & 1, abort_flag, a.status);
+        ok = ok && wait8<BLK>(&sm->s_full[C::kPipe ? ntile & 1 : 0], (C::kPipe ? ntile >> 1 : ntile) & 1, abort_flag, a.status);
         tc_fence_after();
         const uint32_t tS = tmem + (ntile & 1) * N2 + lane_off + h0;
         const int valid = min(kTok, L - t * kTok);
@@ -567,11 +598,23 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
                    : BLK ? fmaf((__uint_as_float(vh[j]) + __uint_as_float(vl[j])) * mul[c + j], sc, lg)
                          : (__uint_as_float(vh[j]) + __uint_as_float(vl[j])) * mul[c + j];
         };
+        // block scales: 16 heads a thread, whose scores stay in registers
+        static_assert(!BLK || HT == 16, "scores in registers");
+        float xs[BLK ? 16 : 1];
+        if constexpr (BLK) load16(0, xs);
+        auto scores16 = [&](int c, float (&x)[16]) {
+          if constexpr (BLK) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = xs[j];
+          } else {
+            load16(c, x);
+          }
+        };
         bool need = first;
 #pragma unroll
         for (int c = 0; c < HT; c += 16) {
           float x[16];
-          load16(c, x);
+          scores16(c, x);
 #pragma unroll
           for (int j = 0; j < 16; ++j) need |= x[j] > m[c + j] + kRaise8;
         }
@@ -585,7 +628,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
 #pragma unroll
           for (int c = 0; c < HT; c += 16) {
             float x[16];
-            load16(c, x);
+            scores16(c, x);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const int k = __reduce_max_sync(0xffffffffu, float_to_ordered(x[j]));
@@ -593,6 +636,11 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
             }
           }
           asm volatile("bar.sync 1, %0;" ::"n"(128 * SG) : "memory");
+          if (C::kPipe && !first) {   // the weighted sum before this tile's may still be adding to O
+            ok = ok && wait8<BLK>(&sm->pv_done, (ntile - 1) & 1, abort_flag, a.status);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+          }
 #pragma unroll
           for (int c = 0; c < HT; c += 16) {
             float alpha[16];
@@ -629,12 +677,13 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
             }
           }
         }
-        // P' = kPScale exp2(s - m) as a hi + lo e4m3 pair, this thread's token column
-        // of P [2 HG heads x 128 tokens] (K-major, 128-byte swizzle)
+        // P' = kPScale exp2(s - m) as e4m3 terms, this thread's token column
+        // of P [terms x HG heads x 128 tokens] (K-major, 128-byte swizzle)
+        uint8_t* pb = pbuf + (C::kPipe ? (ntile & 1) * C::kPBuf : 0);
 #pragma unroll
         for (int c = 0; c < HT; c += 16) {
           float x[16];
-          load16(c, x);
+          scores16(c, x);
           if constexpr (BLK) {
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -647,8 +696,8 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
               terms_e4m3x2<C::kTerms>(p0 * kPScale, p1 * kPScale, term);
 #pragma unroll
               for (int k = 0; k < C::kTerms; ++k) {
-                pbuf[sw128_byte(k * HG + h, row)] = static_cast<uint8_t>(term[k]);
-                pbuf[sw128_byte(k * HG + h + 1, row)] = static_cast<uint8_t>(term[k] >> 8);
+                pb[sw128_byte(k * HG + h, row)] = static_cast<uint8_t>(term[k]);
+                pb[sw128_byte(k * HG + h + 1, row)] = static_cast<uint8_t>(term[k] >> 8);
               }
             }
             continue;
@@ -660,8 +709,8 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
             lsum[c + j] += p;
             uint8_t hi, lo;
             split_e4m3(p * kPScale, hi, lo);
-            pbuf[sw128_byte(h, row)] = hi;
-            pbuf[sw128_byte(HG + h, row)] = lo;
+            pb[sw128_byte(h, row)] = hi;
+            pb[sw128_byte(HG + h, row)] = lo;
           }
         }
         if (!rv) {   // rows outside [start, L) may hold anything (a NaN code): zero them
