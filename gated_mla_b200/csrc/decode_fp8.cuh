@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(256) decode_absorb_fp8_kernel(DecodeArgs a) {
 // ---------------------------------------------------------------------------
 struct Dec8Smem {
   uint64_t full[16], empty[16];   // per ring box
-  uint64_t s_full[2];             // by tile where scores run a tile ahead (kPipe), else the first
-  uint64_t q_full, q_empty, p_full, pv_done, o_done, o_free, drain, never;
+  uint64_t s_full[2], p_full[2], pv_done[2];   // of even and odd tiles where two tiles are in work (kPipe), else the first
+  uint64_t q_full, q_empty, drain2, o_done, o_free, drain, never;
   uint32_t tmem;
   int abort;
   int vote[3];
@@ -215,13 +215,15 @@ struct Dec8Cfg {
   static constexpr int kTerms = BLK ? 3 : 2;                 // e4m3 terms of P'
   static constexpr int kNP = kTerms * HG;                    // columns of P' and of O^T
   static constexpr int kSG = HG >= 32 ? 2 : 1;               // softmax warp groups (head slices)
-  static constexpr int kThreads = 64 + 128 * kSG;
+  static constexpr int kThreads = 64 + 128 * kSG + (BLK && HG == 32 ? 32 : 0);
   static constexpr int kCtasPerSm = HG == 16 ? 2 : 1;
   static constexpr int kQBytes = kNB8 * kN2 * 128;           // 4 boxes of [2 HG rows x 128 B]
-  // Two P buffers where the ring holds two tiles (32 heads, block scales): the scores of
-  // a tile are complete, and its softmax runs, while the weighted sum of the tile before is
-  // still being taken. (With one buffer a tile's softmax and weighted sum took turns:
-  // 575 us for 8 x 131072 tokens and 128 heads.)
+  // Where the ring holds two tiles (32 heads, block scales) there are two P buffers and two
+  // issuing warps, one for the scores and one for the weighted sums: the scores of a tile
+  // are complete, and its softmax runs, while the weighted sum of the tile before is still
+  // being taken. The ring's boxes go in pairs, a barrier each: even a wait for something
+  // complete costs its warp about 250 cycles. (8 x 131072 tokens, 128 heads: in turn 575 us,
+  // two P buffers and one issuing warp 557.)
   static constexpr bool kPipe = BLK && HG == 32;
   static constexpr int kPBuf = ((kNP * 128) + 1023) & ~1023;     // [terms x HG rows x 128 tokens]
   static constexpr int kPBytes = (kPipe ? 2 : 1) * kPBuf;
@@ -230,7 +232,8 @@ struct Dec8Cfg {
   // shared memory of an SM (233472 B) less 1 KB reserved per CTA
   static constexpr int kBudget = kCtasPerSm == 2 ? 233472 / 2 - 1024 : 232448;
   static constexpr int kRingMax = (kBudget - kFixed) / kBox8;
-  static constexpr int kRing = kRingMax > 16 ? 16 : kRingMax;
+  static constexpr int kPair = kPipe ? 2 : 1;                // boxes a barrier
+  static constexpr int kRing = (kRingMax > 16 ? 16 : kRingMax) / kPair * kPair;
   static constexpr int kSmem = kRing * kBox8 + kFixed;
   static constexpr int kTmemCols = 2 * kN2 + 4 * kNP <= 256 ? 256 : 512;   // 2 S^T buffers + 4 O^T chunks
   // the next tile's boxes are probed by the parity of their full barrier, which
@@ -242,10 +245,11 @@ struct Dec8Cfg {
 };
 
 template <int HG, bool BLK>
-__global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 : 1))
+__global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 32 ? 32 : 0), (HG == 16 ? 2 : 1))
     decode_attn_fp8_kernel(const __grid_constant__ DecodeArgs a) {
   using C = Dec8Cfg<HG, BLK>;
-  constexpr int NR = C::kRing, N2 = C::kN2, NP = C::kNP;
+  constexpr int NR = C::kRing, N2 = C::kN2, NP = C::kNP, BP = C::kPair;
+  constexpr int NB = NR / BP;      // barriers of the ring: box c has number c / BP
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem;
@@ -264,10 +268,12 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
     }
     mbar_init(&sm->q_full, 1);
     mbar_init(&sm->q_empty, 1);
-    mbar_init(&sm->s_full[0], 1);
-    mbar_init(&sm->s_full[1], 1);
-    mbar_init(&sm->p_full, 128 * C::kSG);
-    mbar_init(&sm->pv_done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm->s_full[i], 1);
+      mbar_init(&sm->p_full[i], 128 * C::kSG);
+      mbar_init(&sm->pv_done[i], 1);
+    }
+    mbar_init(&sm->drain2, 1);
     mbar_init(&sm->o_done, 1);
     mbar_init(&sm->o_free, 128 * C::kSG);
     mbar_init(&sm->drain, 1);
@@ -327,35 +333,38 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
           page = a.cache.block_table[static_cast<int64_t>(b) * a.cache.max_pages_per_seq + (tok0 + lane * ps) / ps];
         const uint32_t tx = ps >= kTok ? kBox8 : nchunk * ps * 128;
         for (int j = 0; j < kNB8; ++j) {
-          const uint32_t slot = nbox % NR;
-          if (lane == 0) {
-            if (nbox >= static_cast<uint32_t>(NR) &&
-                !wait8<BLK>(&sm->empty[slot], ((nbox / NR) & 1) ^ 1, abort_flag, a.status))
-              ok = false;
-            if (ok) mbar_arrive_expect_tx(&sm->full[slot], tx);
+          const uint32_t slot = nbox % NR, nb = nbox / BP, bs = nb % NB;
+          if (j % BP == 0) {
+            if (lane == 0) {
+              if (nb >= static_cast<uint32_t>(NB) &&
+                  !wait8<BLK>(&sm->empty[bs], ((nb / NB) & 1) ^ 1, abort_flag, a.status))
+                ok = false;
+              if (ok) mbar_arrive_expect_tx(&sm->full[bs], BP * tx);
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
           }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
           uint8_t* dst = ring + slot * kBox8;
           if (!paged) {
-            if (lane == 0) tma_load_2d(&a.cache_map, &sm->full[slot], dst, j * 128, b * a.cache.capacity + tok0, pol_c);
+            if (lane == 0) tma_load_2d(&a.cache_map, &sm->full[bs], dst, j * 128, b * a.cache.capacity + tok0, pol_c);
           } else if (ps >= kTok) {
-            if (lane == 0) tma_load_3d(&a.cache_map, &sm->full[slot], dst, j * 128, tok0 % ps, page, pol_c);
+            if (lane == 0) tma_load_3d(&a.cache_map, &sm->full[bs], dst, j * 128, tok0 % ps, page, pol_c);
           } else if (lane < nchunk) {
-            tma_load_3d(&a.cache_map, &sm->full[slot], dst + lane * ps * 128, j * 128, 0, page, pol_c);
+            tma_load_3d(&a.cache_map, &sm->full[bs], dst + lane * ps * 128, j * 128, 0, page, pol_c);
           }
           ++nbox;
         }
       }
     }
     if (lane == 0 && *abort_flag) {   // let issued copies land before the block exits
-      for (uint32_t c = nbox > static_cast<uint32_t>(NR) ? nbox - NR : 0; c < nbox; ++c)
-        mbar_drain(&sm->full[c % NR], (c / NR) & 1);
+      const uint32_t n = (nbox + BP - 1) / BP;
+      for (uint32_t c = n > static_cast<uint32_t>(NB) ? n - NB : 0; c < n; ++c)
+        mbar_drain(&sm->full[c % NB], (c / NB) & 1);
       if (nq) mbar_drain(&sm->q_full, (nq - 1) & 1);
     }
-  } else if (warp == 1) {
-    // ------------------------------ MMA issuer ------------------------------
-    if constexpr (BLK) {   // the whole warp, converged (see umma_f8_warp)
+  } else if (warp == 1 || (C::kPipe && warp == C::kThreads / 32 - 1)) {
+    // ------------------------------ MMA issuers ------------------------------
+    if constexpr (BLK) {   // whole warps, converged (see umma_f8_warp)
       constexpr uint32_t idS = idesc_e4m3_f32(128, N2, false, false);
       constexpr uint32_t idO = idesc_e4m3_f32(128, NP, true, false);
       const uint32_t ring_a = smem_u32(ring);
@@ -372,56 +381,80 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
         for (int kk = 0; kk < 4; ++kk) umma_f8_warp(tSb, da + kk * 2, db + kk * 2, idS, (j | kk) != 0);
       };
       uint32_t nbox = 0, ntile = 0, nseg = 0;
-      int early = 0;
       bool ok = true;
-      if (a.test_stall && g == 0 && hg == 0) ok = wait(&sm->never, 0);
-      for (int si = seg_lo; si < seg_hi && ok; ++si) {
-        const int4 sg = a.seg_info[si];
-        if (seg_heads(a, sg.x, hg, heads_valid) == 0) continue;
-        ok = wait(&sm->q_full, nseg & 1);
-        // scores of the tile whose first box is number c0, into buffer buf
-        auto scores = [&](uint32_t c0, int from, uint32_t buf) {
-          for (int j = from; j < kNB8 && ok; ++j) {
-            const uint32_t c = c0 + j;
-            ok = wait(&sm->full[c % NR], (c / NR) & 1);
-            if (ok) s_box(c % NR, j, tmem + buf * N2);
-          }
-        };
-        auto weighted_sum = [&](bool first) {
-          tc_fence_after();
-          const uint64_t dPb = dP + (C::kPipe ? (ntile & 1) * (C::kPBuf / 16) : 0);
-#pragma unroll 1
-          for (int j = 0; j < kNB8; ++j) {
-            const uint32_t slot = (nbox + j) % NR;
-            const uint64_t da = dRingMN + slot * (kBox8 / 16);
-#pragma unroll
-            for (int kk = 0; kk < kTok / 32; ++kk)
-              umma_f8_warp(tO + j * NP, da + kk * (4096 / 16), dPb + kk * 2, idO, (!first || kk > 0) ? 1u : 0u);
-            umma_commit_warp(&sm->empty[slot]);
-          }
-        };
-        if (C::kPipe && ok) {
-          scores(nbox, 0, ntile & 1);
-          if (ok && sg.y + 1 == sg.z) umma_commit_warp(&sm->q_empty);
-          if (ok) umma_commit_warp(&sm->s_full[ntile & 1]);
+      // scores of the tile at nbox, its boxes from `from` on, into buffer ntile & 1
+      auto scores = [&](int from) {
+        for (int j = from; j < kNB8 && ok; ++j) {
+          const uint32_t nb = (nbox + j) / BP;
+          if (j % BP == 0) ok = wait(&sm->full[nb % NB], (nb / NB) & 1);
+          if (ok) s_box((nbox + j) % NR, j, tmem + (ntile & 1) * N2);
         }
-        for (int t = sg.y; t < sg.z && ok; ++t, ++ntile) {
-          const bool last = t + 1 == sg.z;
-          if (C::kPipe) {   // the next tile's scores go before this tile's weighted sum
-            if (!last) {
-              scores(nbox + kNB8, 0, (ntile + 1) & 1);
+      };
+      // O^T += C~^T P'^T of the tile at nbox; its boxes are free when this is done
+      auto weighted_sum = [&](bool first) {
+        tc_fence_after();
+        const uint64_t dPb = dP + (C::kPipe ? (ntile & 1) * (C::kPBuf / 16) : 0);
+#pragma unroll 1
+        for (int j = 0; j < kNB8; ++j) {
+          const uint64_t da = dRingMN + (nbox + j) % NR * (kBox8 / 16);
+#pragma unroll
+          for (int kk = 0; kk < kTok / 32; ++kk)
+            umma_f8_warp(tO + j * NP, da + kk * (4096 / 16), dPb + kk * 2, idO, (!first || kk > 0) ? 1u : 0u);
+          if (j % BP == BP - 1) umma_commit_warp(&sm->empty[(nbox + j) / BP % NB]);
+        }
+      };
+      if constexpr (C::kPipe) {
+        const bool sums = warp != 1;
+        if (!sums && a.test_stall && g == 0 && hg == 0) ok = wait(&sm->never, 0);
+        for (int si = seg_lo; si < seg_hi && ok; ++si) {
+          const int4 sg = a.seg_info[si];
+          if (seg_heads(a, sg.x, hg, heads_valid) == 0) continue;
+          if (!sums) ok = wait(&sm->q_full, nseg & 1);
+          for (int t = sg.y; t < sg.z && ok; ++t, ++ntile, nbox += kNB8) {
+            const uint32_t par = (ntile >> 1) & 1;
+            if (!sums) {
+              // the softmax has read the scores of two tiles ago from this buffer
+              if (ntile >= 2) {
+                ok = wait(&sm->p_full[ntile & 1], par ^ 1);
+                tc_fence_after();
+              }
+              if (ok) scores(0);
               if (!ok) break;
-              if (t + 2 == sg.z) umma_commit_warp(&sm->q_empty);
-              umma_commit_warp(&sm->s_full[(ntile + 1) & 1]);
+              if (t + 1 == sg.z) umma_commit_warp(&sm->q_empty);
+              umma_commit_warp(&sm->s_full[ntile & 1]);
+            } else {
+              ok = wait(&sm->p_full[ntile & 1], par);
+              const bool first = t == sg.y;
+              if (ok && first && nseg > 0) ok = wait(&sm->o_free, (nseg - 1) & 1);
+              if (!ok) break;
+              weighted_sum(first);
+              umma_commit_warp(&sm->pv_done[ntile & 1]);
             }
-          } else {
-            scores(nbox, early, ntile & 1);
+          }
+          if (!ok) break;
+          if (sums) umma_commit_warp(&sm->o_done);
+          ++nseg;
+        }
+        if (!ok) {
+          uint64_t* drain = sums ? &sm->drain2 : &sm->drain;
+          umma_commit_warp(drain);
+          mbar_drain(drain, 0);
+        }
+      } else {
+        int early = 0;
+        if (a.test_stall && g == 0 && hg == 0) ok = wait(&sm->never, 0);
+        for (int si = seg_lo; si < seg_hi && ok; ++si) {
+          const int4 sg = a.seg_info[si];
+          if (seg_heads(a, sg.x, hg, heads_valid) == 0) continue;
+          ok = wait(&sm->q_full, nseg & 1);
+          for (int t = sg.y; t < sg.z && ok; ++t) {
+            scores(early);
             if (!ok) break;
-            if (last) umma_commit_warp(&sm->q_empty);
+            if (t + 1 == sg.z) umma_commit_warp(&sm->q_empty);
             umma_commit_warp(&sm->s_full[0]);
             // the next tile's boxes that have landed (a non-blocking probe)
             early = 0;
-            if (!last) {
+            if (t + 1 < sg.z) {
               for (int j = 0; j < kNB8; ++j) {
                 const uint32_t c = nbox + kNB8 + j;
                 if (!__all_sync(0xffffffffu, mbar_test(&sm->full[c % NR], (c / NR) & 1))) break;
@@ -429,22 +462,22 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
                 ++early;
               }
             }
+            ok = wait(&sm->p_full[0], ntile & 1);
+            const bool first = (t == sg.y);
+            if (ok && first && nseg > 0) ok = wait(&sm->o_free, (nseg - 1) & 1);
+            if (!ok) break;
+            weighted_sum(first);
+            nbox += kNB8;
+            ++ntile;
           }
-          ok = wait(&sm->p_full, ntile & 1);
-          const bool first = (t == sg.y);
-          if (ok && first && nseg > 0) ok = wait(&sm->o_free, (nseg - 1) & 1);
           if (!ok) break;
-          weighted_sum(first);
-          if (C::kPipe) umma_commit_warp(&sm->pv_done);
-          nbox += kNB8;
+          umma_commit_warp(&sm->o_done);
+          ++nseg;
         }
-        if (!ok) break;
-        umma_commit_warp(&sm->o_done);
-        ++nseg;
-      }
-      if (!ok) {
-        umma_commit_warp(&sm->drain);
-        mbar_drain(&sm->drain, 0);
+        if (!ok) {
+          umma_commit_warp(&sm->drain);
+          mbar_drain(&sm->drain, 0);
+        }
       }
     } else if (lane == 0) {
       constexpr uint32_t idS = idesc_e4m3_f32(128, N2, false, false);
@@ -488,7 +521,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
               ++early;
             }
           }
-          if (!mbar_wait(&sm->p_full, ntile & 1, abort_flag, a.status)) { ok = false; break; }
+          if (!mbar_wait(&sm->p_full[0], ntile & 1, abort_flag, a.status)) { ok = false; break; }
           const bool first = (t == sg.y);
           if (first && nseg > 0 && !mbar_wait(&sm->o_free, (nseg - 1) & 1, abort_flag, a.status)) { ok = false; break; }
           tc_fence_after();
@@ -637,7 +670,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
           }
           asm volatile("bar.sync 1, %0;" ::"n"(128 * SG) : "memory");
           if (C::kPipe && !first) {   // the weighted sum before this tile's may still be adding to O
-            ok = ok && wait8<BLK>(&sm->pv_done, (ntile - 1) & 1, abort_flag, a.status);
+            ok = ok && wait8<BLK>(&sm->pv_done[(ntile - 1) & 1], ((ntile - 1) >> 1) & 1, abort_flag, a.status);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
           }
@@ -680,6 +713,10 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
         // P' = kPScale exp2(s - m) as e4m3 terms, this thread's token column
         // of P [terms x HG heads x 128 tokens] (K-major, 128-byte swizzle)
         uint8_t* pb = pbuf + (C::kPipe ? (ntile & 1) * C::kPBuf : 0);
+        if (C::kPipe && ntile >= 2) {   // the weighted sum of two tiles ago has read this buffer
+          ok = ok && wait8<BLK>(&sm->pv_done[ntile & 1], ((ntile >> 1) & 1) ^ 1, abort_flag, a.status);
+          ok = __all_sync(0xffffffffu, ok);
+        }
 #pragma unroll
         for (int c = 0; c < HT; c += 16) {
           float x[16];
@@ -723,7 +760,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), (HG == 16 ? 2 :
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&sm->p_full);
+        mbar_arrive(&sm->p_full[C::kPipe ? ntile & 1 : 0]);
         nbox += kNB8;
       }
       // ---- segment end: the partial (O, m, l)
