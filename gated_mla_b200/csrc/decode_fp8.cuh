@@ -19,10 +19,10 @@
 //
 // With one scale s_t for every block of token rows (BLK; c = s_t c~) the weighted
 // sum's weights are p_t s_t, whose spread adds to that of p_t. So the running
-// reference m follows u_t = z_t + log2 s_t, P' = kPScale 2^(u - m) carries the scale
+// reference m follows u_t = z_t + log2 s_t, P' = kPScaleB 2^(u - m) carries the scale
 // into the product, and the softmax sum takes 2^(u - m) / s_t. P' gets a third
 // e4m3 term, and each term is stored 32 times finer than the one before
-// (P' = hi + lo / 32 + lo2 / 1024, in columns of their own): weights 2^-24 below the
+// (P' = hi + lo / 32 + lo2 / 1024, in columns of their own): weights 2^-23 below the
 // largest still count, as they must when one token far outweighs a long
 // context's tail. At N = 3 HG <= 96 an MMA costs what it does at 2 HG.
 //
@@ -45,6 +45,11 @@ constexpr int kDc8 = 512;
 // 2^-15 stay representable.
 constexpr float kRaise8 = 2.f;
 constexpr float kPScale = 64.f;
+// With three terms (block scales) the same P' <= 256 leaves room for a raise only every 5 log2
+// units (a raise rescales O in tensor memory, nearly a tile's time), and weights down to
+// 2^-23 of the largest count.
+constexpr float kRaise8B = 5.f;
+constexpr float kPScaleB = 8.f;
 
 __device__ __forceinline__ uint8_t to_e4m3(float v) {
   return static_cast<uint8_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
@@ -554,7 +559,8 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const int ltid = threadIdx.x - 64;
     const float NEG_INF = -__int_as_float(0x7f800000);
-    const float o_mul = (BLK ? 1.f : a.cache_scale) / kPScale;
+    constexpr float kRaise = BLK ? kRaise8B : kRaise8;
+    const float o_mul = BLK ? 1.f / kPScaleB : a.cache_scale / kPScale;
     uint32_t nbox = 0, ntile = 0, nseg = 0;
     bool ok = true;
     for (int si = seg_lo; si < seg_hi; ++si) {
@@ -649,7 +655,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
           float x[16];
           scores16(c, x);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) need |= x[j] > m[c + j] + kRaise8;
+          for (int j = 0; j < 16; ++j) need |= x[j] > m[c + j] + kRaise;
         }
         const int par = ntile & 1;
         const int vslot = static_cast<int>(ntile % 3u);
@@ -730,7 +736,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
               lsum[c + j] = fmaf(p0, isc, lsum[c + j]);
               lsum[c + j + 1] = fmaf(p1, isc, lsum[c + j + 1]);
               uint32_t term[C::kTerms];
-              terms_e4m3x2<C::kTerms>(p0 * kPScale, p1 * kPScale, term);
+              terms_e4m3x2<C::kTerms>(p0 * kPScaleB, p1 * kPScaleB, term);
 #pragma unroll
               for (int k = 0; k < C::kTerms; ++k) {
                 pb[sw128_byte(k * HG + h, row)] = static_cast<uint8_t>(term[k]);

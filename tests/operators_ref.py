@@ -99,15 +99,17 @@ def gate_values(logits, mode, H, d_h, topk=0):
     return np.repeat(g, d_h, axis=1)
 
 
-def decode(q, c, W_k, W_v, scale):
-    """One query [H, d_h] over rows c [L, d_c]. Returns (o [H, d_h], bound [H, d_h]).
+def decode(q, c, W_k, W_v, scale, s):
+    """One query [H, d_h] over rows c [L, d_c] whose codes have scales s [L]. Returns (o [H, d_h], bound [H, d_h]).
 
     The bound covers the roundings of an FP8 decode, to first order in each:
       * the absorbed query is a sum of two E4M3 terms: relative 2^-4 * 2^-4 an element (and
         2^-19 of the largest, the second term's subnormal step), so a score is off by at
         most d = scale * (2^-8 sum |q_i c_i| + 2^-19 max|q| sum |c_i|), and a weight by a
         factor within e^(2 d) of 1;
-      * three E4M3 terms hold a weight to 2^-12, and to 2^-24 of the largest;
+      * three E4M3 terms, each 32 times finer, hold a weight times its row's scale to 2^-12 (half a
+        step three times: 2^-4 * 2^-4 * 2^-4), and to half the last subnormal step below that:
+        2^-10 / 32^2 of 8 times the reference, which is at most the largest: 2^-23 of it;
       * the latent sum is rounded to bf16 (half a step, 2^-8), and so is the result;
       * fp32 sums of up to L terms, and the hardware exponential and logarithm: 2^-18.
     """
@@ -126,7 +128,7 @@ def decode(q, c, W_k, W_v, scale):
         lat = p @ c
         mag = p @ ac                                     # sum p |c|
         wd = (p * np.expm1(np.minimum(2 * dz, 50))) @ ac + np.abs(lat) * (p @ np.expm1(np.minimum(2 * dz, 50)))
-        d_lat = wd + mag * (2.0 ** -12 + 2.0 ** -18) + 2.0 ** -24 * (p.max() * ac).sum(0) + 2.0 ** -8 * np.abs(lat)
+        d_lat = wd + mag * (2.0 ** -12 + 2.0 ** -18) + 2.0 ** -23 * (p * s).max() * (ac / s[:, None]).sum(0) + 2.0 ** -8 * np.abs(lat)
         o[h] = W_v[h] @ lat
         bound[h] = np.abs(W_v[h]) @ d_lat + 2.0 ** -8 * np.abs(o[h]) + 2.0 ** -18 * (np.abs(W_v[h]) @ np.abs(lat))
     return o, bound

@@ -67,11 +67,12 @@ class Pool:
         assert np.array_equal(self.cache.scales.cpu().numpy().reshape(-1).astype(np.float64), self.scales, equal_nan=True)
 
     def rows(self, b, L):
-        """Rows 0 .. L - 1 of a sequence as values."""
-        out = np.empty((L, D))
+        """Rows 0 .. L - 1 of a sequence as values, and their scales."""
+        out, s = np.empty((L, D)), np.empty(L)
         for p in range(L):
-            out[p] = self.codes[self.row_of(b, p)] * self.scales[self.block_of(b, p)]
-        return out
+            s[p] = self.scales[self.block_of(b, p)]
+            out[p] = self.codes[self.row_of(b, p)] * s[p]
+        return out, s
 
 
 def _latents(T, seed, spread=1.0, tiny=False):
@@ -194,7 +195,8 @@ def _attend(H, lens, page, block, gate="channel", seed=0, q_mul=1.0, spread=1.0,
     gv = (R.gate_values(z.double().cpu().numpy(), gate, H, d_h, topk).reshape(B, H, d_h) if logits else np.ones((B, H, d_h)))
     num = den = 0.0
     for b in range(B) if seqs is None else seqs:
-        ref, bound = R.decode(qq[b], pool.rows(b, lens[b]), wk, wv, 1 / np.sqrt(d_h))
+        c, sc = pool.rows(b, lens[b])
+        ref, bound = R.decode(qq[b], c, wk, wv, 1 / np.sqrt(d_h), sc)
         # the gate: a fast exponential and reciprocal, 2^-20 of the value
         assert np.all(np.abs(got[b] - gv[b] * ref) <= gv[b] * (bound + 2.0 ** -20 * np.abs(ref)) + 1e-30), b
         num += ((got[b] - gv[b] * ref) ** 2).sum()
