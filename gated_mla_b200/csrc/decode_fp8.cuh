@@ -190,6 +190,165 @@ __global__ void __launch_bounds__(256) decode_absorb_fp8_kernel(DecodeArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// The same for a block-scaled cache, on tcgen05: one CTA per (head, 128 latent columns,
+// up to 128 sequences) as decode_absorb_tc; the four column CTAs of a head form a
+// cluster and exchange each sequence's largest |q_lat| through distributed shared
+// memory, since the codes of all 512 columns share one sigma. Latency bound (64
+// sequences, 32 heads: 20 us on CUDA cores, which read W_k once for 8 sequences).
+// Grid (heads + 1, sequence chunks, 4); the last x runs the split plan.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(128) decode_absorb_tc8_kernel(const __grid_constant__ DecodeArgs a) {
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  if (static_cast<int>(blockIdx.x) == a.H) {   // whole clusters
+    if (blockIdx.y == 0 && blockIdx.z == 0) {
+      griddep_wait();
+      decode_plan_block(a);
+    }
+    return;
+  }
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ float s_wmax[4][128], s_max[128], s_inv[128];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int BN = a.absorb_bn;
+  const int nkb = a.d_h / 64;
+  uint8_t* sA = smem;                                  // 2 boxes [d_h rows][64 latent columns]
+  uint8_t* sB = sA + 2 * a.d_h * 128;                  // nkb boxes [BN sequences][64 of d_h]
+  AbsorbSmem* sm = reinterpret_cast<AbsorbSmem*>(sB + nkb * BN * 128);
+  volatile int* abort_flag = &sm->abort;
+  const int h = blockIdx.x, ct = blockIdx.z;
+  const int b0 = blockIdx.y * BN;
+  const int nb = min(BN, a.B - b0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t tcols = BN <= 32 ? 32 : (BN <= 64 ? 64 : 128);
+  if (threadIdx.x == 0) {
+    mbar_init(&sm->full, 1);
+    mbar_init(&sm->mma_done, 1);
+    sm->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&sm->tmem, tcols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem;
+  bool mma_issued = false;   // thread 0
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&a.wk_map);
+    tma_prefetch_desc(&a.q_map);
+    mbar_arrive_expect_tx(&sm->full, 2u * a.d_h * 128 + static_cast<uint32_t>(nkb * BN * 128));
+    for (int j = 0; j < 2; ++j)
+      tma_load_2d(&a.wk_map, &sm->full, sA + j * a.d_h * 128, ct * kAbsorbM + j * 64, h * a.d_h, l2_evict_first());
+  }
+  griddep_wait();   // the queries come from the kernel before this one
+  if (threadIdx.x == 0)
+    for (int kb = 0; kb < nkb; ++kb)
+      tma_load_2d(&a.q_map, &sm->full, sB + kb * BN * 128, h * a.d_h + kb * 64, b0, l2_evict_last());
+  if (threadIdx.x < nb) {   // hard / quantised gates: heads by slot, as decode_absorb_tc
+    int slot = h;
+    float on = 1.f;
+    if (a.gate_hard) {
+      const int b = b0 + threadIdx.x;
+      const float* z = a.gate_logits + static_cast<int64_t>(b) * a.H;
+      int na = 0;
+      slot = head_slot(z, a.H, h, a.gate_mode, a.gate_topk, &na);
+      const float gv = head_gate(z, a.H, h, a.gate_mode, a.gate_topk);
+      on = gv != 0.f ? 1.f : 0.f;
+      if (ct == 0) {
+        a.gvals[static_cast<int64_t>(b) * a.H + h] = gv;
+        a.head_of_slot[static_cast<int64_t>(b) * a.H + slot] = h;
+      }
+    }
+    sm->slot[threadIdx.x] = slot;
+    sm->on[threadIdx.x] = on;
+  }
+  if (threadIdx.x == 0) {
+    if (mbar_poll<0>(&sm->full, 0, abort_flag, a.status)) {
+      tc_fence_after();
+      const uint32_t idesc = idesc_bf16_f32(128, BN, true, false);
+      const uint64_t dA = sdesc_sw128(smem_u32(sA), a.d_h * 128, 1024);
+      const uint64_t dB = sdesc_sw128(smem_u32(sB), 16, 1024);
+      for (int k = 0; k < a.d_h / 16; ++k)
+        umma_bf16(tmem, dA + (k * 2048) / 16, dB + ((k >> 2) * BN * 128 + (k & 3) * 32) / 16, idesc, k != 0);
+      umma_commit(&sm->mma_done);
+      mma_issued = true;
+    } else {
+      mbar_drain(&sm->full, 0);   // copies still in flight land before the block leaves
+    }
+  }
+  __syncthreads();
+  bool ok = !*abort_flag && mbar_poll<0>(&sm->mma_done, 0, abort_flag, a.status);
+  ok = __all_sync(0xffffffffu, ok);
+  // warp w holds latent columns ct*128 + 32 w + lane, one TMEM column per sequence
+  const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+  if (ok) {
+    tc_fence_after();
+    for (int n0 = 0; n0 < BN; n0 += 16) {
+      uint32_t v[16];
+      tmem_ld16(taddr + n0, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {   // magnitudes order as their bits do
+        const uint32_t top = __reduce_max_sync(0xffffffffu, v[j] & 0x7fffffffu);
+        if (lane == 0) s_wmax[warp][n0 + j] = __uint_as_float(top);
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < BN) {
+    const int n = threadIdx.x;
+    s_max[n] = ok ? fmaxf(fmaxf(s_wmax[0][n], s_wmax[1][n]), fmaxf(s_wmax[2][n], s_wmax[3][n])) : 0.f;
+  }
+  cluster_sync_all();
+  if (threadIdx.x < BN) {
+    const int n = threadIdx.x;
+    float mx = 0.f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_map(smem_u32(&s_max[n]), r)) : "memory");
+      mx = fmaxf(mx, v);
+    }
+    const float sigma = mx > 0.f ? mx * a.q_scale / 448.f : 1.f;
+    s_inv[n] = n < nb ? a.q_scale / sigma * sm->on[n] : 0.f;
+    if (ct == 0 && n < nb) a.qmul[static_cast<int64_t>(b0 + n) * a.H + sm->slot[n]] = sigma * a.cache_scale * sm->on[n];
+  }
+  cluster_sync_all();   // every peer has read the maxima; s_inv is written
+  if (ok) {
+    uint8_t* qa = static_cast<uint8_t*>(a.qa);
+    const int c = ct * kAbsorbM + 32 * warp + lane, N2 = 2 * a.HG;
+    for (int n0 = 0; n0 < nb; n0 += 16) {
+      uint32_t v[16];
+      tmem_ld16(taddr + n0, v);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int n = n0 + j;
+        if (n >= nb) break;
+        const int slot = sm->slot[n];
+        // slots past the launched head groups (heads a top-k gate switches off) are never read
+        if (slot >= a.n_hg * a.HG) continue;
+        uint8_t hi, lo;
+        split_e4m3(__uint_as_float(v[j]) * s_inv[n], hi, lo);
+        const int64_t row_hi = (static_cast<int64_t>(b0 + n) * a.n_hg + slot / a.HG) * N2 + slot % a.HG;
+        qa[row_hi * kDc8 + c] = hi;
+        qa[(row_hi + a.HG) * kDc8 + c] = lo;
+      }
+    }
+  } else if (mma_issued) {
+    mbar_drain(&sm->mma_done, 0);   // an issued product completes before TMEM is freed
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tcols);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // attention over the FP8 cache
 // ---------------------------------------------------------------------------
 struct Dec8Smem {

@@ -983,9 +983,20 @@ static cudaError_t launch_attn(const DecodeArgs& a, cudaStream_t st) {
 }
 
 static cudaError_t launch_decode_fp8(DecodeArgs& a, cudaStream_t st) {
-  const int n_absorb = a.H * ((a.B + kAbs8B - 1) / kAbs8B);
-  prof_begin(st, "decode_absorb_plan");
-  cudaError_t e = launch_pdl(decode_absorb_fp8_kernel, dim3(n_absorb + 1), dim3(256), 0, st, 1, a);
+  cudaError_t e;
+  if (a.scales) {
+    const size_t smem = absorb_smem_bytes(a.d_h, a.absorb_bn);
+    e = cudaFuncSetAttribute(decode_absorb_tc8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    prof_begin(st, "decode_absorb_plan");
+    e = launch_pdl(decode_absorb_tc8_kernel, dim3(a.H + 1, (a.B + a.absorb_bn - 1) / a.absorb_bn, 4), dim3(128), smem,
+                   st, 4, a);
+  } else {
+    const int n_absorb = a.H * ((a.B + kAbs8B - 1) / kAbs8B);
+    prof_begin(st, "decode_absorb_plan");
+    e = launch_pdl(decode_absorb_fp8_kernel, dim3(n_absorb + 1), dim3(256), 0, st, 1, a);
+  }
   prof_end(st);
   if (e != cudaSuccess) return e;
   switch (a.HG) {

@@ -648,7 +648,7 @@ static gmla_status decode_impl(const gmla_config* cfg, const gmla_weights* w, co
           : !make_tmap_2d(&a.qa_map, ws + L.off_qa, row, static_cast<uint64_t>(B) * cfg->n_heads,
                           static_cast<uint64_t>(row) * 2, 64, L.HG, true))
     return fail(GMLA_ERR_CUDA, "tensor map for the absorbed queries failed");
-  if (!fp8) {
+  if (!fp8 || cfg->cache_dtype == GMLA_CACHE_FP8_BLOCK) {
     // the tensor-core absorb: W_k as [H*d_h, d_c] in boxes of [d_h x 64], the
     // queries as [B, H*(d_h + d_R)] in boxes of [absorb_bn x 64]
     const int dq = cfg->d_h + cfg->d_rope;
