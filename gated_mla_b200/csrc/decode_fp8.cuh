@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(128) decode_absorb_tc8_kernel(const __grid_con
     return;
   }
   extern __shared__ uint8_t smem_raw[];
-  __shared__ float s_wmax[4][128], s_max[128], s_inv[128];
+  __shared__ float s_wmax[4][128], s_max[128];
+  __shared__ float2 s_row[128];   // 1 / sigma (scaled), and the row of a sequence's hi codes (-1: none)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int BN = a.absorb_bn;
   const int nkb = a.d_h / 64;
@@ -312,29 +313,32 @@ __global__ void __launch_bounds__(128) decode_absorb_tc8_kernel(const __grid_con
       mx = fmaxf(mx, v);
     }
     const float sigma = mx > 0.f ? mx * a.q_scale / 448.f : 1.f;
-    s_inv[n] = n < nb ? a.q_scale / sigma * sm->on[n] : 0.f;
+    int row = -1;
+    if (n < nb) {   // slots past the launched head groups (heads a top-k gate switches off) are never read
+      const int slot = sm->slot[n];
+      if (slot < a.n_hg * a.HG) row = ((b0 + n) * a.n_hg + slot / a.HG) * 2 * a.HG + slot % a.HG;
+    }
+    s_row[n] = make_float2(n < nb ? a.q_scale / sigma * sm->on[n] : 0.f, __int_as_float(row));
     if (ct == 0 && n < nb) a.qmul[static_cast<int64_t>(b0 + n) * a.H + sm->slot[n]] = sigma * a.cache_scale * sm->on[n];
   }
-  cluster_sync_all();   // every peer has read the maxima; s_inv is written
+  cluster_sync_all();   // every peer has read the maxima; s_row is written
   if (ok) {
-    uint8_t* qa = static_cast<uint8_t*>(a.qa);
-    const int c = ct * kAbsorbM + 32 * warp + lane, N2 = 2 * a.HG;
+    uint8_t* qa = static_cast<uint8_t*>(a.qa) + ct * kAbsorbM + 32 * warp + lane;
+    const int lo_off = a.HG * kDc8;
     for (int n0 = 0; n0 < nb; n0 += 16) {
       uint32_t v[16];
       tmem_ld16(taddr + n0, v);
       tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const int n = n0 + j;
-        if (n >= nb) break;
-        const int slot = sm->slot[n];
-        // slots past the launched head groups (heads a top-k gate switches off) are never read
-        if (slot >= a.n_hg * a.HG) continue;
+        const float2 r = s_row[n0 + j];
+        const int row = __float_as_int(r.y);
+        if (row < 0) continue;
         uint8_t hi, lo;
-        split_e4m3(__uint_as_float(v[j]) * s_inv[n], hi, lo);
-        const int64_t row_hi = (static_cast<int64_t>(b0 + n) * a.n_hg + slot / a.HG) * N2 + slot % a.HG;
-        qa[row_hi * kDc8 + c] = hi;
-        qa[(row_hi + a.HG) * kDc8 + c] = lo;
+        split_e4m3(__uint_as_float(v[j]) * r.x, hi, lo);
+        uint8_t* dst = qa + static_cast<int64_t>(row) * kDc8;
+        dst[0] = hi;
+        dst[lo_off] = lo;
       }
     }
   } else if (mma_issued) {
