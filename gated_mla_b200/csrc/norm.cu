@@ -165,19 +165,13 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a) {
       for (int o = 1; o < 32; o <<= 1)
         if (o < g8) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       if (n > 0) {
-        const float part = top * (1.f / 448.f);      // 0 for a group of zeros (or of values too small to scale)
+        const float part = top / 448.f;              // 0 for a group of zeros (or of values too small to divide)
         const float scale = part > 0.f ? part : 1.f;
-        const float mul = 1.f / scale;
         if ((threadIdx.x & (g8 - 1)) == 0) a.scales[row * n_group + e / a.group] = scale;
         uint8_t* c = a.codes + row * a.d + e;
-        // a scale below fp32's normal range has no finite reciprocal: divide there
-        if (!(mul < 3.0e38f)) {
+        // a true division: next to a rounding border a reciprocal's error picks another code
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = y[j] / scale;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] *= mul;
-        }
+        for (int j = 0; j < 8; ++j) y[j] = y[j] / scale;
         uint32_t w[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
