@@ -47,33 +47,25 @@ class LatentCache:
         return self.block_table is not None
 
     def struct(self) -> L.gmla_cache:
-        c = L.gmla_cache()
-        c.data = _p(self.data)
-        c.paged = 1 if self.paged else 0
-        if self.paged:
-            c.batch = self.block_table.shape[0]
-            c.page_size = self.data.shape[1]
-            c.num_pages = self.data.shape[0]
-            c.max_pages_per_seq = self.block_table.shape[1]
-            c.block_table = _p(self.block_table)
-            c.capacity = c.max_pages_per_seq * c.page_size
-        else:
-            c.batch = self.data.shape[0]
-            c.capacity = self.data.shape[1]
-        if self.scales is not None:
-            n, block = self.scales.shape[1], self.scale_block
-            rows = self.data.shape[1]
+        data, table, scales = self.data, self.block_table, self.scales
+        shape = data.shape
+        n, rows = shape[0], shape[1]
+        block = self.scale_block
+        if scales is not None:
             if not block:
-                if not self.paged:
+                if table is None:
                     raise ValueError("a contiguous block-scaled cache needs scale_block")
-                block = rows // max(n, 1)
-            if (self.scales.dtype != torch.float32 or self.scales.device != self.data.device
-                    or self.scales.shape[0] != self.data.shape[0] or block < 1 or n != -(-rows // block)):
+                block = rows // max(scales.shape[1], 1)
+            if (scales.dtype is not torch.float32 or scales.device != data.device or block < 1
+                    or scales.shape != (n, -(-rows // block))):
                 raise ValueError("scales must be float32 [pages, page // block] (paged) or [B, ceil(capacity / block)] "
                                  "on the cache's device")
-            c.scales = _p(self.scales)
-            c.scale_block = block
-        return c
+        else:
+            block = 0
+        if table is None:
+            return L.gmla_cache(_p(data), 0, n, rows, 0, 0, 0, None, _p(scales), block)
+        B, M = table.shape
+        return L.gmla_cache(_p(data), 1, B, M * rows, rows, n, M, _p(table), _p(scales), block)
 
 
 def _check(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: torch.device) -> None:
@@ -129,14 +121,20 @@ def sync_status() -> None:
     _scratch.sync_status()
 
 
-class BatchPlan(NamedTuple):
+class BatchPlan:
     """What one step of a batch over a paged cache needs (see plan_batch)."""
-    seq_lens: torch.Tensor      # int32 [B]: rows of each sequence, the new ones included
-    cu_seqlens: torch.Tensor    # int32 [B + 1]: packed token offsets
-    positions: torch.Tensor     # int32 [n_tokens], -1 behind the last sequence
-    seq_ids: torch.Tensor       # int32 [n_tokens]
-    slots: torch.Tensor         # int64 [n_tokens]: page * page_size + row
-    pages_used: torch.Tensor    # int32 [1]: how many of the free pages were taken
+    __slots__ = ("seq_lens", "cu_seqlens", "positions", "seq_ids", "slots", "pages_used", "_sizes")
+
+    def __init__(self, batch: int, n_tokens: int, device: torch.device):
+        def new(n, dtype=torch.int32):
+            return torch.empty(n, dtype=dtype, device=device)
+        self.seq_lens = new(batch)                      # int32 [B]: rows of each sequence, the new ones included
+        self.cu_seqlens = new(batch + 1)                # int32 [B + 1]: packed token offsets
+        self.positions = new(n_tokens)                  # int32 [n_tokens], -1 behind the last sequence
+        self.seq_ids = new(n_tokens)                    # int32 [n_tokens]
+        self.slots = new(n_tokens, torch.int64)         # int64 [n_tokens]: page * page_size + row
+        self.pages_used = new(1)                        # int32 [1]: how many of the free pages were taken
+        self._sizes = (batch, n_tokens, device)
 
 
 def plan_batch(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -150,30 +148,25 @@ def plan_batch(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     earlier plan of the same sizes. A batch that does not fit is planned as empty and
     reported by ``sync_status``.
     """
-    dev, B, T = cached_lens.device, cached_lens.shape[0], int(n_tokens)
+    dev, B, T = cached_lens.device, cached_lens.shape[0], n_tokens
     stream = _stream_of(cached_lens)
-    i32 = torch.int32
-    _check(cached_lens, "cached_lens", i32, (B,), dev)
-    _check(new_lens, "new_lens", i32, (B,), dev)
     if block_table.dim() != 2 or free_pages.dim() != 1 or T < 0:
         raise ValueError("block_table is [B, max_pages], free_pages [n], n_tokens >= 0")
     M, n_free = block_table.shape[1], free_pages.shape[0]
+    i32 = torch.int32
+    _check(cached_lens, "cached_lens", i32, (B,), dev)
+    _check(new_lens, "new_lens", i32, (B,), dev)
     _check(block_table, "block_table", i32, (B, M), dev)
     _check(free_pages, "free_pages", i32, (n_free,), dev)
     if out is None:
-        new = lambda n, t=i32: torch.empty(n, dtype=t, device=dev)  # noqa: E731
-        out = BatchPlan(new(B), new(B + 1), new(T), new(T), new(T, torch.int64), new(1))
-    else:
-        _check(out.seq_lens, "out.seq_lens", i32, (B,), dev)
-        _check(out.cu_seqlens, "out.cu_seqlens", i32, (B + 1,), dev)
-        _check(out.positions, "out.positions", i32, (T,), dev)
-        _check(out.seq_ids, "out.seq_ids", i32, (T,), dev)
-        _check(out.slots, "out.slots", torch.int64, (T,), dev)
-        _check(out.pages_used, "out.pages_used", i32, (1,), dev)
+        out = BatchPlan(B, T, dev)
+    elif out._sizes != (B, T, dev):
+        raise ValueError(f"out is a plan of {out._sizes}, this batch is {(B, T, dev)}")
     ws = _scratch.get("plan_batch", 256, dev, stream)
-    L.check(L.gmla_plan_batch(_p(cached_lens), _p(new_lens), B, _p(free_pages), n_free, int(page_size), _p(block_table),
-                              M, T, _p(out.seq_lens), _p(out.cu_seqlens), _p(out.positions), _p(out.seq_ids),
-                              _p(out.slots), _p(out.pages_used), ws.data_ptr(), 256, stream), "gmla_plan_batch")
+    L.check(L.lib.gmla_plan_batch(
+        _p(cached_lens), _p(new_lens), B, _p(free_pages), n_free, page_size, _p(block_table), M, T,
+        out.seq_lens.data_ptr(), out.cu_seqlens.data_ptr(), out.positions.data_ptr(), out.seq_ids.data_ptr(),
+        out.slots.data_ptr(), out.pages_used.data_ptr(), ws.data_ptr(), 256, stream), "gmla_plan_batch")
     return out
 
 
@@ -200,11 +193,11 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residua
         raise ValueError("x must be bfloat16 or float32 [T, d]")
     dev, (T, d) = x.device, x.shape
     if out is None and want_out:
-        out = torch.empty(T, d, dtype=x.dtype, device=dev)
+        out = x.new_empty((T, d))
     if residual is None and residual_out is not None:
         raise ValueError("residual_out goes with a residual")
     if residual is not None and residual_out is None:
-        residual_out = torch.empty(T, d, dtype=x.dtype, device=dev)
+        residual_out = x.new_empty((T, d))
     codes = scales = None
     if fp8_group:
         if fp8_group < 0:
