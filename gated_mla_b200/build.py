@@ -24,7 +24,7 @@ BUILD = os.path.join(ROOT, "_build", "gmla")
 LIB = os.path.join(HERE, "libgmla.so")
 SOURCES = ["gmla.cu", "gemm_tc.cu", "decode_tc.cu", "prefill_tc.cu", "simt_f32.cu", "noalloc.cu",
            "plan.cu", "norm.cu", "append.cu", "w4.cu"]
-HEADERS = ["ptx.cuh", "common.cuh", "internal.h", "decode_fp8.cuh", "w4_tc.cuh"]
+HEADERS = ["ptx.cuh", "common.cuh", "internal.h", "decode_fp8.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -72,10 +72,16 @@ __global__ void __launch_bounds__(256) cache_append_kernel(AppendArgs a) {
   const int w = WPL == 1 ? 0 : warp;
   const int blk = a.scale_block;
   int t = unit * a.window;
-  const int total = min(a.cu[a.B], a.T);
+  // one token a sequence, as in a decode step: row t is sequence t's. The offsets that say
+  // so are fetched together, and the row meanwhile
+  const int guess = min(t, a.B - 1);
+  const int cu_end = a.cu[a.B], cu_0 = a.cu[0], cu_g = a.cu[guess], cu_g1 = a.cu[guess + 1];
+  if (w == 0 && t < a.T)
+    prefetch_l2(static_cast<const __nv_bfloat16*>(a.latents) + static_cast<int64_t>(t) * a.stride + lane * 16);
+  const int total = min(cu_end, a.T);
   const int t_end = min(t + a.window, total);
-  if (t >= t_end || t < a.cu[0]) return;   // uniform over the unit
-  int b = find_seq(a.cu, a.B, t, lane);
+  if (t >= t_end || t < cu_0) return;   // uniform over the unit
+  int b = t >= cu_g && t < cu_g1 ? guess : find_seq(a.cu, a.B, t, lane);
   const CacheView& cv = a.cache;
   const int limit = cv.paged ? cv.max_pages_per_seq * cv.page_size : cv.capacity;
   uint8_t* codes = static_cast<uint8_t*>(cv.data);

@@ -145,6 +145,7 @@ struct GemmArgs {
   int32_t kb_per_split;
   int32_t tiles_per_seq;
   int32_t act_seq_stride;
+  int32_t weights_written;       // 1: the weights were written by an earlier kernel of the stream
   const int32_t* cu_seqlens;
   const int32_t* positions;
   const int32_t* seq_ids;

@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(192, kSwap ? 1 : 2) gemm_bf16_tc_kernel(const 
   int64_t* tok_row = reinterpret_cast<int64_t*>(smem + C::kStages * C::kStageBytes + 256);
   int* tok_pos = reinterpret_cast<int*>(tok_row + (kSwap ? BN : 1));
 
-  if (a.row_mode == 1) griddep_wait();   // the tile reads the sequence offsets
+  // the tile reads the sequence offsets, or the weights come from an earlier kernel of the stream
+  if (a.row_mode == 1 || a.weights_written) griddep_wait();
   GemmTile tile;
   if (!gemm_tile<BN, kSwap>(a, tile)) return;   // uniform across the block
 

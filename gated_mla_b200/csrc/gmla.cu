@@ -947,6 +947,39 @@ gmla_status gmla_prefill(const gmla_config* cfg, const gmla_weights* w, const vo
 }
 
 // ---------------------------------------------------------------------------
+// y [T, d_model] = src [T, H*d_h] W^T on the tensor-core GEMM (bf16). weights_written: W
+// comes from an earlier kernel of the stream.
+static gmla_status out_gemm(const gmla_config* cfg, const void* src, int T, const void* W, bool weights_written,
+                            void* y, int* status, cudaStream_t st, const char* name) {
+  const int HD = cfg->n_heads * cfg->d_h, dm = cfg->d_model;
+  if (HD % 8) return fail(GMLA_ERR_UNSUPPORTED, "bf16 path needs H*d_h %% 8 == 0");
+  GemmArgs a{};
+  const bool swap = T <= 256;
+  const SwapPlan sp = gemm_swap_plan((dm + 127) / 128, T, HD, num_sms());
+  const int bn = swap ? sp.bn : 256;
+  const int wtile = gemm_weight_tile(swap, bn);
+  if (!make_tmap_2d(&a.act, src, HD, T, static_cast<uint64_t>(HD) * 2, 64, swap ? bn : 128, true) ||
+      !make_tmap_2d(&a.wt[0], W, HD, dm, static_cast<uint64_t>(HD) * 2, 64, wtile, true))
+    return fail(GMLA_ERR_CUDA, "tensor maps for %s failed", name);
+  a.epi[0] = plain_seg(y, dm, 1 << 30, 0, 0, false, nullptr, false, false);
+  a.seg_rows[0] = dm;
+  a.seg_tile_begin[0] = 0;
+  a.seg_tile_begin[1] = (dm + wtile - 1) / wtile;
+  a.n_seg = 1;
+  a.T = T;
+  a.K = HD;
+  a.row_mode = 0;
+  a.weights_written = weights_written ? 1 : 0;
+  a.status = status;
+  const int ttiles = swap ? sp.ttiles : (T + 127) / 128;
+  if (swap) {
+    a.splits = sp.splits;
+    a.kb_per_split = sp.kb_per_split;
+  }
+  cudaError_t e = launch_gemm_bf16(a, swap, bn, ttiles, st, "gemm_out");
+  return e == cudaSuccess ? GMLA_OK : cuda_fail(e, name);
+}
+
 gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w, const void* o, int32_t T,
                           const float* gate_logits, void* y, void* workspace, size_t workspace_bytes,
                           void* stream) {
@@ -988,40 +1021,16 @@ gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w, const v
     cudaError_t e = launch_gemm_f32(a, st);
     return e == cudaSuccess ? GMLA_OK : cuda_fail(e, "gate_out (fp32)");
   }
-  if (HD % 8) return fail(GMLA_ERR_UNSUPPORTED, "bf16 path needs H*d_h %% 8 == 0");
-  GemmArgs a{};
-  const bool swap = T <= 256;
-  const SwapPlan sp = gemm_swap_plan((dm + 127) / 128, T, HD, num_sms());
-  const int bn = swap ? sp.bn : 256;
-  const int wtile = gemm_weight_tile(swap, bn);
-  if (!make_tmap_2d(&a.act, src, HD, T, static_cast<uint64_t>(HD) * 2, 64, swap ? bn : 128, true) ||
-      !make_tmap_2d(&a.wt[0], w->W_o, HD, dm, static_cast<uint64_t>(HD) * 2, 64, wtile, true))
-    return fail(GMLA_ERR_CUDA, "tensor maps for gate_out failed");
-  a.epi[0] = ep;
-  a.seg_rows[0] = dm;
-  a.seg_tile_begin[0] = 0;
-  a.seg_tile_begin[1] = (dm + wtile - 1) / wtile;
-  a.n_seg = 1;
-  a.T = T;
-  a.K = HD;
-  a.row_mode = 0;
-  a.status = status;
-  const int ttiles = swap ? sp.ttiles : (T + 127) / 128;
-  if (swap) {
-    a.splits = sp.splits;
-    a.kb_per_split = sp.kb_per_split;
-  }
-  cudaError_t e = launch_gemm_bf16(a, swap, bn, ttiles, st, "gemm_out");
-  return e == cudaSuccess ? GMLA_OK : cuda_fail(e, "gate_out");
+  return out_gemm(cfg, src, T, w->W_o, false, y, status, st, "gate_out");
 }
 
 // ---------------------------------------------------------------------------
 constexpr int kW4MaxK = 1 << 24;
 
-// workspace: status word, the activations in the order the kernel reads them, then their
-// group sums among them (few tokens), then the partial tiles (more)
+// workspace: status word; few tokens: the activations in the order the kernel reads them, with
+// their group sums; many: gate ⊙ o [T, K] bf16, then W expanded to bf16 [N, K]
 static size_t w4_act_bytes(const W4Plan& p) {
-  return align256(static_cast<size_t>(p.T8) * p.K256 * 2 + static_cast<size_t>(p.T8) * p.n_chunk * 32);
+  return align256(static_cast<size_t>(p.T8) * (p.K256 * 2 + (p.K256 / kW4Chunk + 1) * 32));
 }
 
 size_t gmla_gate_out_w4_workspace_size(const gmla_config* cfg, int32_t T) {
@@ -1029,7 +1038,7 @@ size_t gmla_gate_out_w4_workspace_size(const gmla_config* cfg, int32_t T) {
   const size_t HD = static_cast<size_t>(cfg->n_heads) * cfg->d_h;
   if (T == 0 || HD > kW4MaxK) return 256;
   const W4Plan p = w4_plan(cfg->d_model, T, static_cast<int>(HD), num_sms());
-  return 256 + w4_act_bytes(p) + static_cast<size_t>(p.G) * 2 * p.bn * 128 * 4;
+  return 256 + w4_act_bytes(p) + (p.nt ? 0 : align256(static_cast<size_t>(cfg->d_model) * HD * 2));
 }
 
 gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const void* o, int32_t T,
@@ -1059,48 +1068,30 @@ gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const vo
   int* status = static_cast<int*>(workspace);
   uint8_t* act = static_cast<uint8_t*>(workspace) + 256;
   const W4Plan plan = w4_plan(N, T, K, sms);
-  if (static_cast<int64_t>(plan.row_tiles) * plan.tok_tiles * plan.n_chunk > (int64_t(1) << 30))
-    return fail(GMLA_ERR_UNSUPPORTED, "gate_out_w4: more than 2^30 tiles of work");
-  float* rest = reinterpret_cast<float*>(act + w4_act_bytes(plan));
+  uint8_t* rest = act + w4_act_bytes(plan);
   const W4PrepArgs p{o,        gate_logits,    act,            T,         K,       cfg->n_heads,
-                     cfg->d_h, cfg->gate_mode, cfg->gate_topk, w4->group, plan.T8, plan.K256, plan.nt, plan.bn};
-  cudaError_t e = launch_w4_prep(p, sms, st);
+                     cfg->d_h, cfg->gate_mode, cfg->gate_topk, w4->group, plan.T8, plan.K256, plan.nt};
+  cudaError_t e = plan.nt || gate_logits ? launch_w4_prep(p, sms, st) : cudaSuccess;
   if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4");
-  CUtensorMap wmap;
-  if (!make_tmap_2d_u8(&wmap, w4->codes, K / 2, N, K / 2, 128, 128))
-    return fail(GMLA_ERR_CUDA, "tensor map for gate_out_w4 failed");
-  const int vec_scales = K % 256 == 0 ? 1 : 0;
-  if (plan.nt) {
-    W4Args a{};
-    a.wmap = wmap;
-    a.x = act;
-    a.scales = w4->scales;
-    a.y = y;
-    a.status = status;
-    a.T = T;
-    a.N = N;
-    a.K = K;
-    a.group = w4->group;
-    a.vec_scales = vec_scales;
-    e = launch_w4_mma(a, plan, st);
-  } else {
-    W4TcArgs a{};
-    a.wmap = wmap;
-    a.x = act;
-    a.scales = w4->scales;
-    a.y = y;
-    a.part = rest;
-    a.status = status;
-    a.T = T;
-    a.N = N;
-    a.K = K;
-    a.group = w4->group;
-    a.vec_scales = vec_scales;
-    a.row_tiles = plan.row_tiles;
-    a.tok_tiles = plan.tok_tiles;
-    a.n_chunk = plan.n_chunk;
-    e = launch_w4_tc(a, plan, st);
+  if (!plan.nt) {
+    const W4ExpandArgs x{w4->codes, w4->scales, rest, N, K, w4->group};
+    e = launch_w4_expand(x, sms, st);
+    if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4: expand");
+    return out_gemm(cfg, gate_logits ? act : o, T, rest, true, y, status, st, "gate_out_w4");
   }
+  W4Args a{};
+  if (!make_tmap_2d_u8(&a.wmap, w4->codes, K / 2, N, K / 2, 128, 128))
+    return fail(GMLA_ERR_CUDA, "tensor map for gate_out_w4 failed");
+  a.x = act;
+  a.scales = w4->scales;
+  a.y = y;
+  a.status = status;
+  a.T = T;
+  a.N = N;
+  a.K = K;
+  a.group = w4->group;
+  a.vec_scales = K % 256 == 0 ? 1 : 0;
+  e = launch_w4_mma(a, plan, st);
   return e == cudaSuccess ? GMLA_OK : cuda_fail(e, "gate_out_w4");
 }
 

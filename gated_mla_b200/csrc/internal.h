@@ -197,8 +197,9 @@ struct PlanArgs {
   int32_t* pages_used;       // [1]
   int* status;
   int32_t B, n_free, page, max_pages, T;
+  int32_t page_shift;        // of a power of two, else -1 (set by the launch)
 };
-cudaError_t launch_plan_batch(const PlanArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_plan_batch(PlanArgs a, int num_sms, cudaStream_t st);
 
 // ----- residual add and root-mean-square norm (norm.cu) -----
 struct NormArgs {
@@ -240,7 +241,7 @@ struct W4PrepArgs {
   const float* gate_logits;  // [T, G] or null
   void* out;                 // in the order the product reads (w4.cu)
   int32_t T, K, H, d_h, gate_mode, gate_topk, group;
-  int32_t T8, K256, nt, bn;  // of the plan
+  int32_t T8, K256, nt;      // of the plan
 };
 struct W4Args {
   CUtensorMap wmap;          // 2D [N, K / 2] bytes
@@ -251,32 +252,21 @@ struct W4Args {
   int32_t T, N, K, group;
   int32_t vec_scales;        // the scales of a 256-k chunk are one aligned load
 };
-struct W4TcArgs {
-  CUtensorMap wmap;          // 2D [N, K / 2] bytes
-  const void* x;             // w4_prep's out
-  const void* scales;        // [N, K / group] bf16
-  void* y;                   // [T, N] bf16
-  float* part;               // [G, 2, BN, 128] partial tiles
-  int* status;
-  int32_t T, N, K, group, vec_scales;
-  int32_t row_tiles, tok_tiles, n_chunk;
-};
-struct W4ReduceArgs {
-  const float* part;
-  void* y;
-  int32_t tiles, n_chunk, tok_tiles, G, BN, N, T;
+struct W4ExpandArgs {
+  const void* codes;
+  const void* scales;
+  void* out;                 // [N, K] bf16
+  int32_t N, K, group;
 };
 struct W4Plan {
-  int nt, splits;            // m16n8k16: token tiles of 8 a CTA (0: tcgen05), K splits
-  int bn, G;                 // tcgen05: tokens a tile, CTAs
-  int row_tiles, tok_tiles, n_chunk;
-  int T8, K256;              // tokens and k rounded up to whole tiles
+  int nt, splits;            // m16n8k16: token columns in tiles of 8, K splits. nt = 0: expansion and GEMM
+  int T8, K256;              // tokens and k, rounded up to whole tiles
 };
-constexpr int kW4MaxMma = 8;
+constexpr int kW4MaxMma = 32;
 W4Plan w4_plan(int N, int T, int K, int num_sms);
 cudaError_t launch_w4_prep(const W4PrepArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_w4_mma(const W4Args& a, const W4Plan& p, cudaStream_t st);
-cudaError_t launch_w4_tc(const W4TcArgs& a, const W4Plan& p, cudaStream_t st);
+cudaError_t launch_w4_expand(const W4ExpandArgs& a, int num_sms, cudaStream_t st);
 
 // ----- elementwise helpers (gmla.cu) -----
 cudaError_t launch_gate_apply(const void* o, const float* g, void* out, int T, int H, int d_h, int gate_mode,

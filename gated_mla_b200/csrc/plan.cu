@@ -64,7 +64,12 @@ __device__ __forceinline__ Pair block_scan2(Pair v, Pair* s_warp, Pair* s_total)
   return r;
 }
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }   // no overflow near 2^31
+// a / page and its ceiling (no overflow near 2^31); page sizes are mostly powers of two
+__device__ __forceinline__ int page_of(const PlanArgs& a, int x) { return a.page_shift >= 0 ? x >> a.page_shift : x / a.page; }
+__device__ __forceinline__ int pages_for(const PlanArgs& a, int x) {
+  const int q = page_of(a, x);
+  return q + (x != q * a.page);
+}
 
 }  // namespace
 
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_batch_kernel(PlanArgs a) {
       bad = true;
       return Pair{0, 0};
     }
-    return Pair{n, ceil_div(c + n, a.page) - ceil_div(c, a.page)};
+    return Pair{n, pages_for(a, c + n) - pages_for(a, c)};
   };
   Pair total{0, 0};
   if (n_chunk > 1) {   // the sums of the whole batch come first: nothing is written for a batch that does not fit
@@ -111,11 +116,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_batch_kernel(PlanArgs a) {
     const int items = (n + kPlanThreads - 1) / kPlanThreads;
     {
       bool bad = false;
-      Pair sum{0, 0};
+      Pair sum{0, 0}, only{0, 0};
       for (int i = 0; i < items; ++i) {
         const int k = tid * items + i;
         if (k < n) {
           const Pair r = request(base + k, bad);
+          only = r;
           sum.tok += r.tok;
           sum.page += r.page;
         }
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_batch_kernel(PlanArgs a) {
         if (k < n) {
           s_cu[k] = static_cast<int>(at.tok);
           s_first[k] = static_cast<int>(at.page);
-          const Pair r = request(base + k, bad);
+          const Pair r = items == 1 ? only : request(base + k, bad);
           at.tok += r.tok;
           at.page += r.page;
         }
@@ -180,10 +186,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_batch_kernel(PlanArgs a) {
           k = x;
           b = base + k;
           cached = a.cached[b];
-          have = ceil_div(cached, a.page);
+          have = pages_for(a, cached);
         }
         const int p = cached + (t - s_cu[k]);
-        const int pi = p / a.page, off = p - pi * a.page;
+        const int pi = page_of(a, p), off = p - pi * a.page;
         int* entry = a.table + static_cast<int64_t>(b) * a.max_pages + pi;
         int page;
         if (pi >= have) {
@@ -217,7 +223,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_batch_kernel(PlanArgs a) {
   }
 }
 
-cudaError_t launch_plan_batch(const PlanArgs& a, int num_sms, cudaStream_t st) {
+cudaError_t launch_plan_batch(PlanArgs a, int num_sms, cudaStream_t st) {
+  a.page_shift = -1;
+  if ((a.page & (a.page - 1)) == 0)
+    for (a.page_shift = 0; (1 << a.page_shift) < a.page;) ++a.page_shift;
   const int per_block = kPlanThreads * kPlanTok;
   int grid = (a.T + per_block - 1) / per_block;
   grid = grid < 1 ? 1 : (grid > 4 * num_sms ? 4 * num_sms : grid);

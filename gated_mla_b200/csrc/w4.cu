@@ -23,7 +23,9 @@
 // K is split over the CTAs of a cluster, which add their fp32 partial tiles
 // through distributed shared memory in a fixed order.
 //
-// More tokens (w4_tc, w4_tc.cuh): the same sums on tcgen05, the codes expanded inside the kernel.
+// Many tokens (above 32): the codes expand once to bf16 in the workspace (w4_expand), which rounds
+// (code - 8) * scale to half a step, 2^-8 relative, as a bf16 weight is; then the tcgen05 GEMM of
+// the bf16 path runs.
 #include "common.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -34,10 +36,9 @@ namespace {
 
 constexpr int kW4Warps = 8;               // consumer warps; one more issues the copies
 constexpr int kW4Threads = 32 * (kW4Warps + 1);
-// 16-row tiles a warp, which would share each activation fragment: two (and two CTAs an SM
-// instead of three) took 21.6 us against 21.8 at 7168 x 16384, but 8.2 against 6.9 at 4096 x 4096.
-constexpr int kW4Tiles = 1;
-constexpr int kW4Rows = 16 * kW4Tiles * kW4Warps;   // weight rows per CTA
+// One 16-row tile a warp. (Two, which share each activation fragment, with two CTAs an SM instead
+// of three, took 21.6 us against 21.8 at 7168 x 16384, one token, but 8.2 against 6.9 at 4096 x 4096.)
+constexpr int kW4Rows = 16 * kW4Warps;    // weight rows per CTA
 constexpr int kW4WBytes = kW4Rows * 128;  // codes of a stage: 128 bytes (256 k) a row
 
 __device__ __forceinline__ uint32_t w4_pair(uint32_t w, int i) {   // (128 + v_i, 128 + v_{i+4}) as bf16x2
@@ -73,42 +74,38 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-constexpr int kW4CtasPerSm = 3;           // by their shared memory
+// CTAs that share an SM, by their shared memory and registers
+constexpr int w4_ctas_per_sm(int nt) { return nt <= 2 ? 3 : 2; }
 
 struct W4Smem {
   uint64_t full[4], empty[4];
   int abort;
 };
 
+template <int NT>   // token columns in tiles of 8: 1, 2 or 4
 struct W4Cfg {
-  static constexpr int kXFrag = (kW4Chunk / 32) * 512;         // [8 steps of 32 k][32 lanes][16 bytes]
-  static constexpr int kXBytes = kXFrag + 256;                 // then -136 sums [groups of the chunk, up to 8][8] fp32
-  static constexpr int kStage = (kW4WBytes + kXBytes + 1023) & ~1023;
+  static constexpr int kXFrag = (kW4Chunk / 32) * NT * 512;    // [8 steps of 32 k][NT][32 lanes][16 bytes]
+  static constexpr int kXBytes = kXFrag + 256 * NT;            // then -136 sums [groups of the chunk, up to 8][8 NT] fp32
   static constexpr int kStages = 3;
+  // the codes' boxes first (1024-byte aligned for the swizzle), then the activations
   static constexpr int kPitch = kW4Rows + 4;                   // floats between tokens of the partial tile
-  static constexpr int kRed = kPitch * 8 * 4;                  // fp32 partial tile, over the ring once it has drained
-  static constexpr int kRing = kStage * kStages > kRed ? kStage * kStages : kRed;
+  static constexpr int kRed = kPitch * 8 * NT * 4;             // fp32 partial tile, over the ring once it has drained
+  static constexpr int kRing = kStages * (kW4WBytes + kXBytes) > kRed ? kStages * (kW4WBytes + kXBytes) : kRed;
   static constexpr int kSmem = kRing + 1024 + static_cast<int>(sizeof(W4Smem));
-  static constexpr int kCtas = kW4CtasPerSm;
+  static constexpr int kCtas = w4_ctas_per_sm(NT);
   static_assert(kStages <= 4, "barriers");
+  static_assert(kRing % 8 == 0, "barriers behind the ring");
   static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory of the CTAs sharing an SM");
 };
 
 }  // namespace
 
-}  // namespace gmla
-
-#include "w4_tc.cuh"
-
-namespace gmla {
-
 // ---------------------------------------------------------------------------
 // a = gate ⊙ o in bf16, in fragment order, and -136 times its sum over each group.
-// out: for each chunk of 256 k, [8 steps][g * 4 + c][8 bf16]: token g, k = 32 step + 8 c +
-// (0 4 1 5 2 6 3 7), then the sums [256 / group][8] fp32 in 256 bytes. Tokens and k behind
+// out: for each chunk of 256 k, [8 steps][nt][g * 4 + c][8 bf16]: token 8 n + g, k = 32 step + 8 c +
+// (0 4 1 5 2 6 3 7), then the sums [256 / group][8 nt] fp32 in 256 nt bytes. Tokens and k behind
 // the end are zeros. A thread makes one run of 8 k; the runs of a group are neighbouring
-// lanes. nt = 0 (for w4_tc): out is the image of the swizzled shared-memory
-// tiles [T8 / bn][K256 / 64][bn][128 bytes], the runs of 8 in the same order, and no sums are made.
+// lanes. nt = 0 (for the GEMM): out is [T, K] as it is, and no sums are made.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
   griddep_wait();
@@ -146,40 +143,39 @@ __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
           w[j] = pack_bf16x2(__uint_as_float(w[j] << 16) * g[2 * j], __uint_as_float(w[j] & 0xffff0000u) * g[2 * j + 1]);
       }
     }
+    if (a.nt == 0) {
+      if (i < n) reinterpret_cast<uint4*>(a.out)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      continue;
+    }
     uint4 r;
     r.x = __byte_perm(w[0], w[2], 0x5410);
     r.y = __byte_perm(w[0], w[2], 0x7632);
     r.z = __byte_perm(w[1], w[3], 0x5410);
     r.w = __byte_perm(w[1], w[3], 0x7632);
-    if (a.nt == 0) {
-      const int tb = t / a.bn, tn = t % a.bn;
-      const int64_t at = ((static_cast<int64_t>(tb) * (a.K256 >> 6) + (k >> 6)) * a.bn + tn) * 8 + (((k >> 3) ^ tn) & 7);
-      if (i < n) reinterpret_cast<uint4*>(a.out)[at] = r;
-      continue;
-    }
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
     for (int o = 1; o < g8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (i < n) {
-      uint8_t* blk = static_cast<uint8_t*>(a.out) + static_cast<int64_t>(k / kW4Chunk) * W4Cfg::kXBytes;
+      uint8_t* blk = static_cast<uint8_t*>(a.out) + static_cast<int64_t>(k / kW4Chunk) * (a.nt * W4Cfg<1>::kXBytes);
       if (k % a.group == 0)
-        reinterpret_cast<float*>(blk + W4Cfg::kXFrag)[k % kW4Chunk / a.group * 8 + t] = -136.f * sum;
-      reinterpret_cast<uint4*>(blk)[((k >> 5) & 7) * 32 + t * 4 + ((k >> 3) & 3)] = r;
+        reinterpret_cast<float*>(blk + a.nt * W4Cfg<1>::kXFrag)[k % kW4Chunk / a.group * 8 * a.nt + t] = -136.f * sum;
+      reinterpret_cast<uint4*>(blk)[(((k >> 5) & 7) * a.nt + (t >> 3)) * 32 + (t & 7) * 4 + ((k >> 3) & 3)] = r;
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// few tokens (up to 8). Grid (row tiles, 1, K splits); the splits of a tile form a cluster. GPC groups per 256-k chunk (8, 4 or 2).
+// few tokens (up to 8 NT). Grid (row tiles, 1, K splits); the splits of a tile form a cluster.
+// GPC groups per 256-k chunk (8, 4 or 2).
 // ---------------------------------------------------------------------------
-template <int GPC>
-__global__ void __launch_bounds__(kW4Threads, W4Cfg::kCtas) w4_mma_kernel(const __grid_constant__ W4Args a) {
-  using C = W4Cfg;
-  constexpr int MT = kW4Tiles;
+template <int NT, int GPC>
+__global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(const __grid_constant__ W4Args a) {
+  using C = W4Cfg<NT>;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring_x = ring + NS * kW4WBytes;
   W4Smem* sm = reinterpret_cast<W4Smem*>(ring + C::kRing);
   volatile int* abort_flag = &sm->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -199,11 +195,11 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg::kCtas) w4_mma_kernel(const 
   __syncthreads();
   if (threadIdx.x == 0) griddep_launch_dependents();
 
-  float acc[MT][4];
+  float acc[NT][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[m][j] = 0.f;
+    for (int j = 0; j < 4; ++j) acc[n][j] = 0.f;
 
   int issued = 0;   // stages requested (copy thread)
   if (warp == kW4Warps) {
@@ -217,11 +213,11 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg::kCtas) w4_mma_kernel(const 
       auto load_w = [&](int i) {
         const int s = i % NS;
         mbar_arrive_expect_tx(&sm->full[s], kW4WBytes + C::kXBytes);
-        tma_load_2d(&a.wmap, &sm->full[s], ring + s * C::kStage, (rank + i * splits) * 128, row0, pol_w);
+        tma_load_2d(&a.wmap, &sm->full[s], ring + s * kW4WBytes, (rank + i * splits) * 128, row0, pol_w);
       };
       auto load_x = [&](int i) {
         const int s = i % NS;
-        bulk_load(ring + s * C::kStage + kW4WBytes, x + static_cast<int64_t>(rank + i * splits) * C::kXBytes, C::kXBytes,
+        bulk_load(ring_x + s * C::kXBytes, x + static_cast<int64_t>(rank + i * splits) * C::kXBytes, C::kXBytes,
                   &sm->full[s], pol_x);
       };
       for (int i = 0; i < pre; ++i) load_w(i);
@@ -237,101 +233,92 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg::kCtas) w4_mma_kernel(const 
   } else {
     const int g = lane >> 2, c = lane & 3;
     const int n_groups = a.K / a.group;
-    const __nv_bfloat16* sc[MT][2];
+    const __nv_bfloat16* sc[2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = row0 + (warp * MT + m) * 16 + g + 8 * h;
-        sc[m][h] = static_cast<const __nv_bfloat16*>(a.scales) + static_cast<int64_t>(row < a.N ? row : 0) * n_groups;
-      }
+    for (int h = 0; h < 2; ++h) {
+      const int row = row0 + warp * 16 + g + 8 * h;
+      sc[h] = static_cast<const __nv_bfloat16*>(a.scales) + static_cast<int64_t>(row < a.N ? row : 0) * n_groups;
+    }
     // the scales of a chunk's groups, one chunk ahead of their use
-    uint32_t next[MT][2][GPC / 2];
+    uint32_t next[2][GPC / 2];
     auto load_scales = [&](int chunk) {
       const int first = chunk * GPC;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const __nv_bfloat16* p = sc[m][h] + first;
-          uint32_t(&to)[GPC / 2] = next[m][h];
-          if (a.vec_scales) {
-            if constexpr (GPC == 8) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-              to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
-            } else if constexpr (GPC == 4) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-              to[0] = v.x, to[1] = v.y;
-            } else {
-              to[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-            }
+      for (int h = 0; h < 2; ++h) {
+        const __nv_bfloat16* p = sc[h] + first;
+        if (a.vec_scales) {
+          if constexpr (GPC == 8) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+            next[h][0] = v.x, next[h][1] = v.y, next[h][2] = v.z, next[h][3] = v.w;
+          } else if constexpr (GPC == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+            next[h][0] = v.x, next[h][1] = v.y;
           } else {
+            next[h][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+          }
+        } else {
 #pragma unroll
-            for (int j = 0; j < GPC / 2; ++j) {   // groups behind K scale nothing (their activations are zeros)
-              const uint32_t lo = first + 2 * j < n_groups ? __bfloat16_as_ushort(p[2 * j]) : 0;
-              const uint32_t hi = first + 2 * j + 1 < n_groups ? __bfloat16_as_ushort(p[2 * j + 1]) : 0;
-              to[j] = lo | (hi << 16);
-            }
+          for (int j = 0; j < GPC / 2; ++j) {   // groups behind K scale nothing (their activations are zeros)
+            const uint32_t lo = first + 2 * j < n_groups ? __bfloat16_as_ushort(p[2 * j]) : 0;
+            const uint32_t hi = first + 2 * j + 1 < n_groups ? __bfloat16_as_ushort(p[2 * j + 1]) : 0;
+            next[h][j] = lo | (hi << 16);
           }
         }
+      }
     };
     if (n_c > 0) load_scales(rank);
-    // rows g and g + 8 of a 16-row tile: word c of the 16-byte chunk j ^ g
-    const uint32_t w_off = (warp * MT * 16 + g) * 128 + (g << 4) + 4 * c;
+    // rows g and g + 8 of the warp's 16: word c of the 16-byte chunk j ^ g
+    const uint32_t w_off = (warp * 16 + g) * 128 + (g << 4) + 4 * c;
     for (int i = 0; i < n_c; ++i) {
       const int s = i % NS;
-      uint32_t cur[MT][2][GPC / 2];
+      uint32_t cur[2][GPC / 2];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < GPC / 2; ++j) cur[m][h][j] = next[m][h][j];
+        for (int j = 0; j < GPC / 2; ++j) cur[h][j] = next[h][j];
       if (i + 1 < n_c) load_scales(rank + (i + 1) * splits);
       bool ok = mbar_poll<20>(&sm->full[s], (i / NS) & 1, abort_flag, a.status);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const uint8_t* ws = ring + s * C::kStage;
-      const uint8_t* xs = ws + kW4WBytes + lane * 16;
+      const uint8_t* ws = ring + s * kW4WBytes;
+      const uint8_t* xs = ring_x + s * C::kXBytes;
       constexpr int JPG = 8 / GPC;     // 32-k steps per group
 #pragma unroll
       for (int gr = 0; gr < GPC; ++gr) {
-        const float2 corr = *reinterpret_cast<const float2*>(ws + kW4WBytes + C::kXFrag + (gr * 8 + 2 * c) * 4);
-        // two chains of products: the latency of a warp's chain, not issue, sets its pace
-        float part[MT][4], part2[MT][4];
+        float part[NT][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          part[m][0] = corr.x, part[m][1] = corr.y, part[m][2] = corr.x, part[m][3] = corr.y;
-          part2[m][0] = part2[m][1] = part2[m][2] = part2[m][3] = 0.f;
+        for (int n = 0; n < NT; ++n) {
+          const float2 corr = *reinterpret_cast<const float2*>(xs + C::kXFrag + (gr * 8 * NT + n * 8 + 2 * c) * 4);
+          part[n][0] = corr.x, part[n][1] = corr.y, part[n][2] = corr.x, part[n][3] = corr.y;
         }
 #pragma unroll
         for (int jj = 0; jj < JPG; ++jj) {
           const int j = gr * JPG + jj;         // 16 bytes of codes a row; lane c takes word c: k = 32 j + 8 c ..
-          const uint4 x = *reinterpret_cast<const uint4*>(xs + j * 512);
           const uint8_t* wp = ws + (w_off ^ (j << 4));
+          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wp);
+          const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wp + 1024);
+          uint32_t f0[4], f1[4];
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint32_t w0 = *reinterpret_cast<const uint32_t*>(wp + m * 2048);
-            const uint32_t w1 = *reinterpret_cast<const uint32_t*>(wp + m * 2048 + 1024);
-            uint32_t f0[4], f1[4];
+          for (int q = 0; q < 4; ++q) {
+            f0[q] = w4_pair(w0, q);
+            f1[q] = w4_pair(w1, q);
+          }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              f0[q] = w4_pair(w0, q);
-              f1[q] = w4_pair(w1, q);
-            }
-            mma_16816(part[m], f0[0], f1[0], f0[1], f1[1], x.x, x.y);
-            mma_16816(part2[m], f0[2], f1[2], f0[3], f1[3], x.z, x.w);
+          for (int n = 0; n < NT; ++n) {
+            const uint4 x = *reinterpret_cast<const uint4*>(xs + (j * NT + n) * 512 + lane * 16);
+            mma_16816(part[n], f0[0], f1[0], f0[1], f1[1], x.x, x.y);
+            mma_16816(part[n], f0[2], f1[2], f0[3], f1[3], x.z, x.w);
           }
         }
+        const uint32_t u0 = cur[0][gr >> 1], u1 = cur[1][gr >> 1];
+        const float s0 = __uint_as_float((gr & 1) ? (u0 & 0xffff0000u) : (u0 << 16));
+        const float s1 = __uint_as_float((gr & 1) ? (u1 & 0xffff0000u) : (u1 << 16));
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint32_t u0 = cur[m][0][gr >> 1], u1 = cur[m][1][gr >> 1];
-          const float s0 = __uint_as_float((gr & 1) ? (u0 & 0xffff0000u) : (u0 << 16));
-          const float s1 = __uint_as_float((gr & 1) ? (u1 & 0xffff0000u) : (u1 << 16));
-          acc[m][0] = fmaf(part[m][0] + part2[m][0], s0, acc[m][0]);
-          acc[m][1] = fmaf(part[m][1] + part2[m][1], s0, acc[m][1]);
-          acc[m][2] = fmaf(part[m][2] + part2[m][2], s1, acc[m][2]);
-          acc[m][3] = fmaf(part[m][3] + part2[m][3], s1, acc[m][3]);
+        for (int n = 0; n < NT; ++n) {
+          acc[n][0] = fmaf(part[n][0], s0, acc[n][0]);
+          acc[n][1] = fmaf(part[n][1], s0, acc[n][1]);
+          acc[n][2] = fmaf(part[n][2], s1, acc[n][2]);
+          acc[n][3] = fmaf(part[n][3], s1, acc[n][3]);
         }
       }
       __syncwarp();
@@ -345,15 +332,14 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg::kCtas) w4_mma_kernel(const 
     __syncthreads();
   }
   griddep_wait();   // y may still be read by an earlier kernel
-  // every copy has landed and been read: the ring becomes the partial tile [8 tokens][rows]
+  // every copy has landed and been read: the ring becomes the partial tile [8 NT tokens][rows]
   float* red = reinterpret_cast<float*>(ring);
   if (warp < kW4Warps) {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        red[(2 * c + (j & 1)) * C::kPitch + (warp * MT + m) * 16 + g + 8 * (j >> 1)] = acc[m][j];
+      for (int j = 0; j < 4; ++j) red[(n * 8 + 2 * c + (j & 1)) * C::kPitch + warp * 16 + g + 8 * (j >> 1)] = acc[n][j];
   }
   if (splits > 1)
     cluster_sync_all();
@@ -391,53 +377,80 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg::kCtas) w4_mma_kernel(const 
 }
 
 // ---------------------------------------------------------------------------
+// bf16((code - 8) * scale), 32 codes a thread: bound by the bytes that it writes
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) w4_expand_kernel(W4ExpandArgs a) {
+  griddep_wait();   // the workspace may still be read by an earlier product
+  griddep_launch_dependents();
+  const int k32 = a.K >> 5;
+  const int64_t n = static_cast<int64_t>(a.N) * k32;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t row = i / k32;
+    const int k = static_cast<int>(i - row * k32) * 32;
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.codes) + row * (a.K >> 1) + (k >> 1));
+    const float s = __bfloat162float(static_cast<const __nv_bfloat16*>(a.scales)[row * (a.K / a.group) + k / a.group]);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * a.K + k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t r[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float v0 = static_cast<float>(static_cast<int>((w[j] >> (8 * q)) & 15u) - 8);
+        const float v1 = static_cast<float>(static_cast<int>((w[j] >> (8 * q + 4)) & 15u) - 8);
+        r[q] = pack_bf16x2(v0 * s, v1 * s);
+      }
+      dst[j] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-template <int GPC>
+template <int NT, int GPC>
 static cudaError_t launch_w4(const W4Args& a, int splits, cudaStream_t st) {
-  auto k = w4_mma_kernel<GPC>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, W4Cfg::kSmem);
+  using C = W4Cfg<NT>;
+  auto k = w4_mma_kernel<NT, GPC>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid((a.N + kW4Rows - 1) / kW4Rows, 1, splits);
   prof_begin(st, "w4_mma");
-  e = launch_pdl(k, grid, dim3(kW4Threads), W4Cfg::kSmem, st, splits, a);
+  e = launch_pdl(k, grid, dim3(kW4Threads), C::kSmem, st, splits, a);
   prof_end(st);
   return e;
 }
 
-// Up to kW4MaxMma tokens on m16n8k16, more on tcgen05 (at 7168 x 16384, 8 tokens: 22.5 us
-// against 28.0).
-//
-// m16n8k16: K splits: the number (1 .. 8, one cluster) with the least time, counted as
-// waves of resident CTAs times the chunks that each works through plus about two chunks'
-// time for its start and its sum.
-// tcgen05: token tile the smallest of 16 .. 128 that holds T; one CTA per SM.
+template <int NT>
+static cudaError_t launch_w4_group(const W4Args& a, int splits, cudaStream_t st) {
+  switch (a.group) {
+    case 32: return launch_w4<NT, 8>(a, splits, st);
+    case 64: return launch_w4<NT, 4>(a, splits, st);
+    default: return launch_w4<NT, 2>(a, splits, st);
+  }
+}
+
+// Token columns: the smallest of 8, 16 and 32 that holds T; more tokens are left to expansion
+// and GEMM. K splits: the number (1 .. 8, one cluster) with the least time, counted as waves of
+// resident CTAs times the chunks that each works through plus about two chunks' time for its
+// start and its sum.
 W4Plan w4_plan(int N, int T, int K, int num_sms) {
   W4Plan p{};
+  p.T8 = T;
+  p.K256 = K;
+  if (T > kW4MaxMma) return p;
   const int chunks = (K + kW4Chunk - 1) / kW4Chunk;
-  p.n_chunk = chunks;
-  if (T > kW4MaxMma) {
-    const int64_t row_tiles = (N + 127) / 128;
-    p.row_tiles = static_cast<int>(row_tiles);
-    p.bn = T <= 16 ? 16 : (T <= 32 ? 32 : (T <= 64 ? 64 : 128));
-    p.tok_tiles = (T + p.bn - 1) / p.bn;
-    const int64_t U = row_tiles * p.tok_tiles * chunks;
-    p.G = static_cast<int>(U < num_sms ? U : num_sms);
-    p.T8 = p.tok_tiles * p.bn;
-    p.K256 = chunks * kW4Chunk;
-    return p;
-  }
-  p.nt = 1;
-  p.tok_tiles = 1;
-  p.row_tiles = (N + kW4Rows - 1) / kW4Rows;
-  const int64_t slots = static_cast<int64_t>(num_sms) * kW4CtasPerSm;
+  p.nt = T <= 8 ? 1 : (T <= 16 ? 2 : 4);
+  const int64_t tiles = (N + kW4Rows - 1) / kW4Rows;
+  const int64_t slots = static_cast<int64_t>(num_sms) * w4_ctas_per_sm(p.nt);
   int64_t best = 0;
   for (int s = 1; s <= 8 && s <= chunks; ++s) {
-    const int64_t cost = ((static_cast<int64_t>(p.row_tiles) * s + slots - 1) / slots) * ((chunks + s - 1) / s + 2);
+    const int64_t cost = ((tiles * s + slots - 1) / slots) * ((chunks + s - 1) / s + 2);
     if (s == 1 || cost < best) best = cost, p.splits = s;
   }
+  p.T8 = 8 * p.nt;
   p.K256 = chunks * kW4Chunk;
-  p.T8 = 8;
   return p;
 }
 
@@ -452,55 +465,19 @@ cudaError_t launch_w4_prep(const W4PrepArgs& a, int num_sms, cudaStream_t st) {
 }
 
 cudaError_t launch_w4_mma(const W4Args& a, const W4Plan& p, cudaStream_t st) {
-  switch (a.group) {
-    case 32: return launch_w4<8>(a, p.splits, st);
-    case 64: return launch_w4<4>(a, p.splits, st);
-    default: return launch_w4<2>(a, p.splits, st);
+  switch (p.nt) {
+    case 1: return launch_w4_group<1>(a, p.splits, st);
+    case 2: return launch_w4_group<2>(a, p.splits, st);
+    default: return launch_w4_group<4>(a, p.splits, st);
   }
 }
 
-template <int BN, int MPG>
-static cudaError_t launch_tc(const W4TcArgs& a, int G, cudaStream_t st) {
-  using C = W4TcCfg<BN>;
-  auto k = w4_tc_kernel<BN, MPG>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
-  prof_begin(st, "w4_tc");
-  e = launch_pdl(k, dim3(G), dim3(C::kThreads), C::kSmem, st, 1, a);
-  prof_end(st);
-  return e;
-}
-
-template <int BN>
-static cudaError_t launch_tc_group(const W4TcArgs& a, int G, cudaStream_t st) {
-  switch (a.group) {
-    case 32: return launch_tc<BN, 2>(a, G, st);
-    case 64: return launch_tc<BN, 4>(a, G, st);
-    default: return launch_tc<BN, 8>(a, G, st);
-  }
-}
-
-cudaError_t launch_w4_tc(const W4TcArgs& a, const W4Plan& p, cudaStream_t st) {
-  cudaError_t e;
-  switch (p.bn) {
-    case 16: e = launch_tc_group<16>(a, p.G, st); break;
-    case 32: e = launch_tc_group<32>(a, p.G, st); break;
-    case 64: e = launch_tc_group<64>(a, p.G, st); break;
-    default: e = launch_tc_group<128>(a, p.G, st); break;
-  }
-  if (e != cudaSuccess) return e;
-  W4ReduceArgs r{};
-  r.part = a.part;
-  r.y = a.y;
-  r.tiles = p.row_tiles * p.tok_tiles;
-  r.n_chunk = p.n_chunk;
-  r.tok_tiles = p.tok_tiles;
-  r.G = p.G;
-  r.BN = p.bn;
-  r.N = a.N;
-  r.T = a.T;
-  prof_begin(st, "w4_reduce");
-  e = launch_pdl(w4_reduce_kernel, dim3(r.tiles, p.bn / 8), dim3(128), 0, st, 1, r);
+cudaError_t launch_w4_expand(const W4ExpandArgs& a, int num_sms, cudaStream_t st) {
+  const int64_t n = static_cast<int64_t>(a.N) * (a.K / 32);
+  const int64_t want = (n + 255) / 256;
+  const int grid = static_cast<int>(want < 16LL * num_sms ? want : 16LL * num_sms);
+  prof_begin(st, "w4_expand");
+  cudaError_t e = launch_pdl(w4_expand_kernel, dim3(grid), dim3(256), 0, st, 1, a);
   prof_end(st);
   return e;
 }
