@@ -23,7 +23,7 @@
 // K is split over the CTAs of a cluster, which add their fp32 partial tiles
 // through distributed shared memory in a fixed order.
 //
-// Many tokens (above 32): the codes expand once to bf16 in the workspace (w4_expand), which rounds
+// Many tokens (above 64): the codes expand once to bf16 in the workspace (w4_expand), which rounds
 // (code - 8) * scale to half a step, 2^-8 relative, as a bf16 weight is; then the tcgen05 GEMM of
 // the bf16 path runs.
 #include "common.cuh"
@@ -102,7 +102,7 @@ struct W4Cfg {
 
 // ---------------------------------------------------------------------------
 // a = gate ⊙ o in bf16, in fragment order, and -136 times its sum over each group.
-// out: for each chunk of 256 k, [8 steps][nt][g * 4 + c][8 bf16]: token 8 n + g, k = 32 step + 8 c +
+// out: for each token tile of 8 nt and each chunk of 256 k, [8 steps][nt][g * 4 + c][8 bf16]: token 8 n + g of the tile, k = 32 step + 8 c +
 // (0 4 1 5 2 6 3 7), then the sums [256 / group][8 nt] fp32 in 256 nt bytes. Tokens and k behind
 // the end are zeros. A thread makes one run of 8 k; the runs of a group are neighbouring
 // lanes. nt = 0 (for the GEMM): out is [T, K] as it is, and no sums are made.
@@ -157,16 +157,18 @@ __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
     for (int j = 0; j < 4; ++j) sum += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
     for (int o = 1; o < g8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (i < n) {
-      uint8_t* blk = static_cast<uint8_t*>(a.out) + static_cast<int64_t>(k / kW4Chunk) * (a.nt * W4Cfg<1>::kXBytes);
+      const int tile = t / (8 * a.nt), tt = t - tile * (8 * a.nt);
+      uint8_t* blk = static_cast<uint8_t*>(a.out) +
+                     (static_cast<int64_t>(tile) * (a.K256 / kW4Chunk) + k / kW4Chunk) * (a.nt * W4Cfg<1>::kXBytes);
       if (k % a.group == 0)
-        reinterpret_cast<float*>(blk + a.nt * W4Cfg<1>::kXFrag)[k % kW4Chunk / a.group * 8 * a.nt + t] = -136.f * sum;
-      reinterpret_cast<uint4*>(blk)[(((k >> 5) & 7) * a.nt + (t >> 3)) * 32 + (t & 7) * 4 + ((k >> 3) & 3)] = r;
+        reinterpret_cast<float*>(blk + a.nt * W4Cfg<1>::kXFrag)[k % kW4Chunk / a.group * 8 * a.nt + tt] = -136.f * sum;
+      reinterpret_cast<uint4*>(blk)[(((k >> 5) & 7) * a.nt + (tt >> 3)) * 32 + (tt & 7) * 4 + ((k >> 3) & 3)] = r;
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// few tokens (up to 8 NT). Grid (row tiles, 1, K splits); the splits of a tile form a cluster.
+// few tokens, tiles of 8 NT. Grid (row tiles, token tiles, K splits); the splits of a tile form a cluster.
 // GPC groups per 256-k chunk (8, 4 or 2).
 // ---------------------------------------------------------------------------
 template <int NT, int GPC>
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
       tma_prefetch_desc(&a.wmap);
       const uint64_t pol_w = l2_evict_first(), pol_x = l2_evict_last();
       const int pre = n_c < NS ? n_c : NS;
-      const uint8_t* x = static_cast<const uint8_t*>(a.x);
+      const uint8_t* x = static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(blockIdx.y) * n_chunk * C::kXBytes;
       auto load_w = [&](int i) {
         const int s = i % NS;
         mbar_arrive_expect_tx(&sm->full[s], kW4WBytes + C::kXBytes);
@@ -348,7 +350,8 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
   // CTA `rank` adds up its share of the tile's rows, four at a time, over the splits in order
   const int q_lo = (kW4Rows / 4) * rank / splits, q_n = (kW4Rows / 4) * (rank + 1) / splits - q_lo;
   const uint32_t red_addr = smem_u32(red);
-  for (int i = threadIdx.x; i < a.T * q_n; i += kW4Threads) {
+  const int t0 = blockIdx.y * 8 * NT, n_t = a.T - t0 < 8 * NT ? a.T - t0 : 8 * NT;
+  for (int i = threadIdx.x; i < n_t * q_n; i += kW4Threads) {
     const int t = i / q_n, r = (q_lo + i % q_n) * 4;
     if (row0 + r >= a.N) continue;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
     } else {
       v = *reinterpret_cast<const float4*>(red + t * C::kPitch + r);
     }
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + static_cast<int64_t>(t) * a.N + row0 + r;
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + static_cast<int64_t>(t0 + t) * a.N + row0 + r;
     if (a.N % 4 == 0) {
       *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     } else {
@@ -410,29 +413,29 @@ __global__ void __launch_bounds__(256) w4_expand_kernel(W4ExpandArgs a) {
 // host side
 // ---------------------------------------------------------------------------
 template <int NT, int GPC>
-static cudaError_t launch_w4(const W4Args& a, int splits, cudaStream_t st) {
+static cudaError_t launch_w4(const W4Args& a, const W4Plan& p, cudaStream_t st) {
   using C = W4Cfg<NT>;
   auto k = w4_mma_kernel<NT, GPC>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.N + kW4Rows - 1) / kW4Rows, 1, splits);
+  const dim3 grid((a.N + kW4Rows - 1) / kW4Rows, p.T8 / (8 * NT), p.splits);
   prof_begin(st, "w4_mma");
-  e = launch_pdl(k, grid, dim3(kW4Threads), C::kSmem, st, splits, a);
+  e = launch_pdl(k, grid, dim3(kW4Threads), C::kSmem, st, p.splits, a);
   prof_end(st);
   return e;
 }
 
 template <int NT>
-static cudaError_t launch_w4_group(const W4Args& a, int splits, cudaStream_t st) {
+static cudaError_t launch_w4_group(const W4Args& a, const W4Plan& p, cudaStream_t st) {
   switch (a.group) {
-    case 32: return launch_w4<NT, 8>(a, splits, st);
-    case 64: return launch_w4<NT, 4>(a, splits, st);
-    default: return launch_w4<NT, 2>(a, splits, st);
+    case 32: return launch_w4<NT, 8>(a, p, st);
+    case 64: return launch_w4<NT, 4>(a, p, st);
+    default: return launch_w4<NT, 2>(a, p, st);
   }
 }
 
-// Token columns: the smallest of 8, 16 and 32 that holds T; more tokens are left to expansion
-// and GEMM. K splits: the number (1 .. 8, one cluster) with the least time, counted as waves of
+// Token columns: the smallest of 8, 16 and 32 that holds T, or two tiles of 32, which share a row
+// tile's codes in L2; more tokens are left to expansion and GEMM. K splits: the number (1 .. 8, one cluster) with the least time, counted as waves of
 // resident CTAs times the chunks that each works through plus about two chunks' time for its
 // start and its sum.
 W4Plan w4_plan(int N, int T, int K, int num_sms) {
@@ -442,14 +445,15 @@ W4Plan w4_plan(int N, int T, int K, int num_sms) {
   if (T > kW4MaxMma) return p;
   const int chunks = (K + kW4Chunk - 1) / kW4Chunk;
   p.nt = T <= 8 ? 1 : (T <= 16 ? 2 : 4);
-  const int64_t tiles = (N + kW4Rows - 1) / kW4Rows;
+  const int token_tiles = (T + 8 * p.nt - 1) / (8 * p.nt);
+  const int64_t tiles = static_cast<int64_t>((N + kW4Rows - 1) / kW4Rows) * token_tiles;
   const int64_t slots = static_cast<int64_t>(num_sms) * w4_ctas_per_sm(p.nt);
   int64_t best = 0;
   for (int s = 1; s <= 8 && s <= chunks; ++s) {
     const int64_t cost = ((tiles * s + slots - 1) / slots) * ((chunks + s - 1) / s + 2);
     if (s == 1 || cost < best) best = cost, p.splits = s;
   }
-  p.T8 = 8 * p.nt;
+  p.T8 = 8 * p.nt * token_tiles;
   p.K256 = chunks * kW4Chunk;
   return p;
 }
@@ -466,9 +470,9 @@ cudaError_t launch_w4_prep(const W4PrepArgs& a, int num_sms, cudaStream_t st) {
 
 cudaError_t launch_w4_mma(const W4Args& a, const W4Plan& p, cudaStream_t st) {
   switch (p.nt) {
-    case 1: return launch_w4_group<1>(a, p.splits, st);
-    case 2: return launch_w4_group<2>(a, p.splits, st);
-    default: return launch_w4_group<4>(a, p.splits, st);
+    case 1: return launch_w4_group<1>(a, p, st);
+    case 2: return launch_w4_group<2>(a, p, st);
+    default: return launch_w4_group<4>(a, p, st);
   }
 }
 
