@@ -262,7 +262,7 @@ struct W4Plan {
   int nt, splits;            // m16n8k16: token columns in tiles of 8, K splits. nt = 0: expansion and GEMM
   int T8, K256;              // tokens and k, rounded up to whole tiles
 };
-constexpr int kW4MaxMma = 64;
+constexpr int kW4MaxMma = 256;
 W4Plan w4_plan(int N, int T, int K, int num_sms);
 cudaError_t launch_w4_prep(const W4PrepArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_w4_mma(const W4Args& a, const W4Plan& p, cudaStream_t st);

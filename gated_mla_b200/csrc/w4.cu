@@ -23,7 +23,7 @@
 // K is split over the CTAs of a cluster, which add their fp32 partial tiles
 // through distributed shared memory in a fixed order.
 //
-// Many tokens (above 64): the codes expand once to bf16 in the workspace (w4_expand), which rounds
+// Many tokens (above 256): the codes expand once to bf16 in the workspace (w4_expand), which rounds
 // (code - 8) * scale to half a step, 2^-8 relative, as a bf16 weight is; then the tcgen05 GEMM of
 // the bf16 path runs.
 #include "common.cuh"
@@ -434,10 +434,14 @@ static cudaError_t launch_w4_group(const W4Args& a, const W4Plan& p, cudaStream_
   }
 }
 
-// Token columns: the smallest of 8, 16 and 32 that holds T, or two tiles of 32, which share a row
-// tile's codes in L2; more tokens are left to expansion and GEMM. K splits: the number (1 .. 8, one cluster) with the least time, counted as waves of
-// resident CTAs times the chunks that each works through plus about two chunks' time for its
-// start and its sum.
+// Token columns: the smallest of 8, 16 and 32 that holds T, or up to eight tiles of 32, which share a
+// row tile's codes in L2. More tokens are left to expansion and GEMM (us at 4096 x 4096 and 7168 x
+// 16384: 64 tokens 16.7 and 80 against 27 and 123, 128 tokens 24 and 133 against 35 and 153, 256 tokens
+// 39 and 240 against 53 and 264). K splits: the number (1 .. 8, one cluster) with the least time,
+// counted as waves of resident CTAs times the chunks that each works through plus about two chunks'
+// time for its start and its sum. A cluster stays within one GPC, so the last slots cannot all be
+// filled: a thirty-second is left out (288 CTAs of 296 in clusters of 3 ran as two waves, 31 us, where
+// clusters of 2 take 22).
 W4Plan w4_plan(int N, int T, int K, int num_sms) {
   W4Plan p{};
   p.T8 = T;
@@ -447,7 +451,7 @@ W4Plan w4_plan(int N, int T, int K, int num_sms) {
   p.nt = T <= 8 ? 1 : (T <= 16 ? 2 : 4);
   const int token_tiles = (T + 8 * p.nt - 1) / (8 * p.nt);
   const int64_t tiles = static_cast<int64_t>((N + kW4Rows - 1) / kW4Rows) * token_tiles;
-  const int64_t slots = static_cast<int64_t>(num_sms) * w4_ctas_per_sm(p.nt);
+  const int64_t slots = static_cast<int64_t>(num_sms) * w4_ctas_per_sm(p.nt) * 31 / 32;
   int64_t best = 0;
   for (int s = 1; s <= 8 && s <= chunks; ++s) {
     const int64_t cost = ((tiles * s + slots - 1) / slots) * ((chunks + s - 1) / s + 2);

@@ -261,7 +261,7 @@ GMLA_API gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w
  *   o, T, gate_logits, y: as gmla_gate_out (bf16 dtype only)
  *   workspace    gmla_gate_out_w4_workspace_size(cfg, T) bytes; calls that may
  *                overlap need workspaces of their own
- * Up to 64 tokens the codes are multiplied as they are and the scale is applied in
+ * Up to 256 tokens the codes are multiplied as they are and the scale is applied in
  * fp32: no weight is rounded. Above that the weights are expanded to bf16 in the
  * workspace once a call (each rounded once, as a bf16 weight is).
  * ------------------------------------------------------------------------- */
