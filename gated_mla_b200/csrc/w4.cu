@@ -436,12 +436,13 @@ static cudaError_t launch_w4_group(const W4Args& a, const W4Plan& p, cudaStream_
 
 // Token columns: the smallest of 8, 16 and 32 that holds T, or up to eight tiles of 32, which share a
 // row tile's codes in L2. More tokens are left to expansion and GEMM (us at 4096 x 4096 and 7168 x
-// 16384: 64 tokens 16.7 and 80 against 27 and 123, 128 tokens 24 and 133 against 35 and 153, 256 tokens
-// 39 and 240 against 53 and 264). K splits: the number (1 .. 8, one cluster) with the least time,
+// 16384: 64 tokens 16.7 and 72 against 27 and 123, 128 tokens 24 and 136 against 35 and 153, 256 tokens
+// 39 and 230 against 53 and 264). K splits: the number (1 .. 8, one cluster) with the least time,
 // counted as waves of resident CTAs times the chunks that each works through plus about two chunks'
-// time for its start and its sum. A cluster stays within one GPC, so the last slots cannot all be
-// filled: a thirty-second is left out (288 CTAs of 296 in clusters of 3 ran as two waves, 31 us, where
-// clusters of 2 take 22).
+// time for its start and its sum. A cluster stays within one GPC, of which some have fewer SMs, and
+// w4_prep's last CTAs still hold slots when it is placed: an eighth of the slots is left out. (One
+// token at 7168 x 16384: 392 of 444 CTAs, in clusters of 7, took 22 us in a stream but two waves and
+// 36 us in a graph; 336, in clusters of 6, take 23 and 25. 32 tokens: clusters of 5 51 us, of 4 41.)
 W4Plan w4_plan(int N, int T, int K, int num_sms) {
   W4Plan p{};
   p.T8 = T;
@@ -451,7 +452,7 @@ W4Plan w4_plan(int N, int T, int K, int num_sms) {
   p.nt = T <= 8 ? 1 : (T <= 16 ? 2 : 4);
   const int token_tiles = (T + 8 * p.nt - 1) / (8 * p.nt);
   const int64_t tiles = static_cast<int64_t>((N + kW4Rows - 1) / kW4Rows) * token_tiles;
-  const int64_t slots = static_cast<int64_t>(num_sms) * w4_ctas_per_sm(p.nt) * 31 / 32;
+  const int64_t slots = static_cast<int64_t>(num_sms) * w4_ctas_per_sm(p.nt) * 7 / 8;
   int64_t best = 0;
   for (int s = 1; s <= 8 && s <= chunks; ++s) {
     const int64_t cost = ((tiles * s + slots - 1) / slots) * ((chunks + s - 1) / s + 2);
