@@ -217,7 +217,7 @@ struct NormArgs {
   float eps;
 };
 cudaError_t launch_add_rms_norm(NormArgs a, bool f32, int num_sms, cudaStream_t st);
-int norm_vectors(int d, int T, int num_sms);
+int norm_vectors(int d, int T, bool f32, int num_sms);
 constexpr int kNormMaxD = 32768;   // 32 warps of 4 vectors
 
 // ----- append to a block-scaled FP8 cache (append.cu) -----

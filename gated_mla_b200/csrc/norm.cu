@@ -70,13 +70,23 @@ __device__ __forceinline__ void store8(float* p, int n, bool vec, const float (&
   }
 }
 
+// Registers a thread. The bf16 forms wait for HBM with their loads in flight, so rows resident count
+// for more than the few words spilled (16384 rows of 7168, four vectors: 161 us with 56 registers, 165
+// with 52, 176 with 64; of 4096, two vectors and no codes: 84 us with 32, 89 with 40, 109 with the
+// weights loaded early and 64; of 2048, one vector: 47 us with 32, 53 with 40). fp32 rows have twice
+// the bytes in flight.
+// 1024 threads of 64 are what a block may hold.
+constexpr int norm_regs(int vpt, bool f32, bool grp) {
+  return f32 ? 64 : (vpt == 4 ? 56 : (vpt == 2 && grp ? 40 : 32));
+}
+
 }  // namespace
 
 // One row per `warps` warps; VPT vectors of 8 elements a thread (vector i of lane t
 // covers elements 8 (i * 32 * warps + t) ..). blockDim = warps * 32 * rows a block.
 // VEC: d and the row strides allow 16-byte accesses, and every vector is whole.
 template <typename T, int VPT, bool VEC, bool GRP>
-__global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a) {
+__global__ void __maxnreg__(norm_regs(VPT, sizeof(T) == 4, GRP)) add_rms_norm_kernel(NormArgs a) {
   __shared__ float s_sum[32];
   griddep_wait();
   griddep_launch_dependents();
@@ -91,7 +101,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a) {
   T* out = static_cast<T*>(a.out) + row * a.out_stride;
   const T* wt = static_cast<const T*>(a.weight);
   float v[VPT][8], w8[VPT][8];
-  // every load of the row, then the weights (held for after the reduction)
+  // every load of the row, then, in the form for few rows, the weights (held for after the reduction)
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int e = (i * tpr + lane_r) * 8;
@@ -113,7 +123,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a) {
       }
     }
   }
-  if (VPT <= 2 && wt) {
+  if (VPT == 1 && wt) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int e = (i * tpr + lane_r) * 8;
@@ -151,7 +161,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = v[i][j] * inv;
     if (n > 0 && wt) {
-      if (VPT > 2) load8<T>(wt + e, n, VEC, w8[i]);
+      if (VPT > 1) load8<T>(wt + e, n, VEC, w8[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] *= w8[i][j];
     }
@@ -208,7 +218,7 @@ static cudaError_t launch_norm_t(const NormArgs& a, int vpt, dim3 grid, dim3 blo
 
 cudaError_t launch_add_rms_norm(NormArgs a, bool f32, int num_sms, cudaStream_t st) {
   const int nvec = (a.d + 7) / 8;
-  const int vpt = norm_vectors(a.d, a.T, num_sms);
+  const int vpt = norm_vectors(a.d, a.T, f32, num_sms);
   a.warps = (nvec + 32 * vpt - 1) / (32 * vpt);
   const int rows = a.warps >= 8 ? 1 : 8 / a.warps;       // rows a block (256 threads or one row)
   const dim3 block(a.warps * 32 * rows);
@@ -221,12 +231,12 @@ cudaError_t launch_add_rms_norm(NormArgs a, bool f32, int num_sms, cudaStream_t 
 
 // Vectors a thread. Few rows: as few as 32 warps allow (the shortest chain: 8 rows of 7168
 // take 2.6 us with one, 3.8 with four). Many: about 8 warps a row, so that an SM holds
-// several rows in different phases (16384 rows of 7168: 176 us with four, 0.82 of the HBM
-// rate, 210 with two, 191 with one; of 2048: 51, 56 and 47).
-int norm_vectors(int d, int T, int num_sms) {
+// several rows in different phases (16384 rows of 7168: 161 us with four, 0.90 of the HBM
+// rate, 167 with two, 188 with one; in fp32 293 with four, 274 with two).
+int norm_vectors(int d, int T, bool f32, int num_sms) {
   const int nvec = (d + 7) / 8;
   if (T <= 2 * num_sms) return nvec <= 1024 ? 1 : (nvec <= 2048 ? 2 : 4);
-  return nvec <= 256 ? 1 : (nvec <= 512 ? 2 : 4);
+  return nvec <= 256 ? 1 : (nvec <= (f32 ? 1024 : 512) ? 2 : 4);
 }
 
 }  // namespace gmla
