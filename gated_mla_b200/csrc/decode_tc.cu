@@ -999,6 +999,9 @@ static cudaError_t launch_decode_fp8(DecodeArgs& a, cudaStream_t st) {
   }
   prof_end(st);
   if (e != cudaSuccess) return e;
+  // Block scales: neither the attention nor the merge begins before its predecessor has ended. Begun
+  // early, the three kernels took, in a graph, 118 us instead of 112 (64 sequences, paged), 510 instead
+  // of 503 (8 of 128k rows) and 27 instead of 25 (one short sequence).
   switch (a.HG) {
     case 16: e = a.scales ? launch_attn_fp8<16, true>(a, st) : launch_attn_fp8<16, false>(a, st); break;
     case 32: e = a.scales ? launch_attn_fp8<32, true>(a, st) : launch_attn_fp8<32, false>(a, st); break;
@@ -1006,7 +1009,7 @@ static cudaError_t launch_decode_fp8(DecodeArgs& a, cudaStream_t st) {
   }
   if (e != cudaSuccess) return e;
   prof_begin(st, "decode_merge");
-  e = launch_pdl(decode_merge_kernel, dim3(a.H, a.B), dim3(128), 0, st, 1, a);
+  e = launch_pdl(decode_merge_kernel, dim3(a.H, a.B), dim3(128), 0, st, 1, a, !a.scales);
   prof_end(st);
   return e;
 }

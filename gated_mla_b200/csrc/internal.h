@@ -18,10 +18,11 @@ int check_config(const ::gmla_config* c);
 // Launches `kernel` with programmatic stream serialization: it may begin
 // while the previous kernel of the stream is still running, and calls
 // griddep_wait() before it touches data another kernel reads or writes. With
-// cluster_z > 1 the blocks form clusters of that size along z.
+// cluster_z > 1 the blocks form clusters of that size along z. early = false: it begins
+// when the previous kernel has ended.
 template <typename Args>
 inline cudaError_t launch_pdl(void (*kernel)(Args), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                              int cluster_z, const Args& args) {
+                              int cluster_z, const Args& args, bool early = true) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -30,7 +31,7 @@ inline cudaError_t launch_pdl(void (*kernel)(Args), dim3 grid, dim3 block, size_
   cudaLaunchAttribute attr[2];
   int n = 0;
   attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[n].val.programmaticStreamSerializationAllowed = 1;
+  attr[n].val.programmaticStreamSerializationAllowed = early ? 1 : 0;
   ++n;
   if (cluster_z > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
