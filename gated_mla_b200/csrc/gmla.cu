@@ -132,6 +132,13 @@ gmla_status check_ptr(const void* p, const char* name, bool required = true) {
   return GMLA_OK;
 }
 
+// Request lengths and lists of pages are read word by word, so a batch or a pool may be a slice.
+gmla_status check_words(const void* p, const char* name, bool required) {
+  if (!p) return required ? fail(GMLA_ERR_INVALID_ARG, "%s is NULL", name) : GMLA_OK;
+  if (reinterpret_cast<uintptr_t>(p) % 4) return fail(GMLA_ERR_INVALID_ARG, "%s is not 4-byte aligned", name);
+  return GMLA_OK;
+}
+
 #define GMLA_TRY(x)                         \
   do {                                      \
     gmla_status _s = (x);                   \
@@ -1113,9 +1120,9 @@ gmla_status gmla_plan_batch(const int32_t* cached_lens, const int32_t* new_lens,
   if (static_cast<int64_t>(page_size) * max_pages_per_seq > (int64_t(1) << 31) - 1)
     return fail(GMLA_ERR_UNSUPPORTED, "a sequence of more than 2^31 - 1 rows");
   GMLA_TRY(check_status_workspace(workspace, workspace_bytes, "plan_batch"));
-  GMLA_TRY(check_ptr(cached_lens, "cached_lens", B > 0));
-  GMLA_TRY(check_ptr(new_lens, "new_lens", B > 0));
-  GMLA_TRY(check_ptr(free_pages, "free_pages", n_free > 0));
+  GMLA_TRY(check_words(cached_lens, "cached_lens", B > 0));
+  GMLA_TRY(check_words(new_lens, "new_lens", B > 0));
+  GMLA_TRY(check_words(free_pages, "free_pages", n_free > 0));
   GMLA_TRY(check_ptr(block_table, "block_table", B > 0));
   GMLA_TRY(check_ptr(seq_lens, "seq_lens", B > 0));
   GMLA_TRY(check_ptr(cu_seqlens, "cu_seqlens"));

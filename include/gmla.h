@@ -279,6 +279,7 @@ GMLA_API size_t gmla_gate_out_w4_workspace_size(const gmla_config* cfg, int32_t 
  *   new_lens     [B] int32: tokens each sequence gets in this step (0 is allowed)
  *   free_pages   [n_free] int32: unused page ids; the first *pages_used are taken,
  *                in the order of the sequences
+ *   (these three may start at any element, so a batch or a pool may be a slice)
  *   block_table  [B, max_pages_per_seq] int32, in and out: entries of the pages that
  *                a sequence's new rows begin are written, all others are left as they were
  *   T            token rows of the outputs (>= the sum of new_lens)

@@ -41,7 +41,8 @@ def _plan(L, **kw):
 @pytest.mark.parametrize("bad", [dict(B=-1), dict(T=-1), dict(n_free=-1), dict(page_size=0), dict(max_pages_per_seq=0),
                                  dict(cached_lens=None), dict(new_lens=None), dict(free_pages=None), dict(block_table=None),
                                  dict(seq_lens=None), dict(cu_seqlens=None), dict(positions=P + 4), dict(slots=P + 8),
-                                 dict(seq_ids=None), dict(pages_used=None)])
+                                 dict(seq_ids=None), dict(pages_used=None), dict(cached_lens=P + 1), dict(new_lens=P + 2),
+                                 dict(free_pages=P + 2)])
 def test_plan_batch(L, bad):
     assert _plan(L, **bad) == L.GMLA_ERR_INVALID_ARG
 
