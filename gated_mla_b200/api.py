@@ -99,12 +99,16 @@ class _Scratch:
     def get(self, key: str, nbytes: int, device: torch.device, stream: int) -> torch.Tensor:
         """At least `nbytes` bytes whose status word was zeroed when they were made."""
         capturing = torch.cuda.is_current_stream_capturing()
-        ws = None if capturing else self._held.get((key, device.index, stream))
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            if not capturing:
-                self._held[(key, device.index, stream)] = ws
+        held = None if capturing else self._held.get((key, device.index, stream))
+        if held is not None and held.numel() >= nbytes:
+            return held
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if held is None:
             L.check(L.gmla_clear_status(ws.data_ptr(), stream), "clear_status")
+        else:
+            ws[:4].copy_(held[:4])       # what it has recorded stays to be reported
+        if not capturing:
+            self._held[(key, device.index, stream)] = ws
         return ws
 
     def sync_status(self) -> None:
@@ -117,7 +121,8 @@ _scratch = _Scratch()
 
 
 def sync_status() -> None:
-    """Synchronise and raise if a plan_batch call reported a batch that cannot be."""
+    """Synchronise and raise if a plan_batch call reported a batch that cannot be. Calls captured
+    into a graph have workspaces of their own, which this does not read."""
     _scratch.sync_status()
 
 

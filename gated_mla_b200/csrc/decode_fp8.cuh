@@ -26,9 +26,13 @@
 // largest still count, as they must when one token far outweighs a long
 // context's tail. At N = 3 HG <= 96 an MMA costs what it does at 2 HG.
 //
-// Kernels: decode_absorb_fp8 (q_lat, its scale and hi/lo codes; its last block
-// builds the split plan as decode_absorb_plan does), decode_attn_fp8 (below),
-// then decode_merge and the W_v GEMM of the bf16 path.
+// Kernels: decode_absorb_fp8, with block scales decode_absorb_tc8 (q_lat, its scale and
+// hi/lo codes; its last block builds the split plan as decode_absorb_plan does),
+// decode_attn_fp8 (below), then decode_merge and the W_v GEMM of the bf16 path.
+//
+// Block scales, attention alone: 64 paged sequences, 32 heads 85 us, where reading the codes takes
+// 35; 8 sequences of 131072 rows, 128 heads 483 us, of which the MMAs of the three-term product
+// and the tile's softmax take turns (the codes take 88).
 #pragma once
 #include <cuda_fp8.h>
 

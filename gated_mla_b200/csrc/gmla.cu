@@ -1082,7 +1082,7 @@ gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const vo
   if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4");
   if (!plan.nt) {
     const W4ExpandArgs x{w4->codes, w4->scales, rest, N, K, w4->group};
-    e = launch_w4_expand(x, sms, st);
+    e = launch_w4_expand(x, st);
     if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4: expand");
     return out_gemm(cfg, gate_logits ? act : o, T, rest, true, y, status, st, "gate_out_w4");
   }

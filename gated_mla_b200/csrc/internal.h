@@ -267,7 +267,7 @@ constexpr int kW4MaxMma = 256;
 W4Plan w4_plan(int N, int T, int K, int num_sms);
 cudaError_t launch_w4_prep(const W4PrepArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_w4_mma(const W4Args& a, const W4Plan& p, cudaStream_t st);
-cudaError_t launch_w4_expand(const W4ExpandArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_w4_expand(const W4ExpandArgs& a, cudaStream_t st);
 
 // ----- elementwise helpers (gmla.cu) -----
 cudaError_t launch_gate_apply(const void* o, const float* g, void* out, int T, int H, int d_h, int gate_mode,

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
   const int g8 = a.group >> 3;
   for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x; i0 < n; i0 += stride) {   // uniform over a block
     const int64_t i = i0 + threadIdx.x;
-    const int t = static_cast<int>(i / k8);
+    const int t = n >> 32 ? static_cast<int>(i / k8) : static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(k8));
     const int k = static_cast<int>(i - static_cast<int64_t>(t) * k8) * 8;
     uint32_t w[4] = {0, 0, 0, 0};
     const bool live = i < n && t < a.T && k < a.K;
@@ -380,32 +380,28 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
 }
 
 // ---------------------------------------------------------------------------
-// bf16((code - 8) * scale), 32 codes a thread: bound by the bytes that it writes
+// bf16((code - 8) * scale), 8 codes a thread, one row a block: bound by the bytes that it writes
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) w4_expand_kernel(W4ExpandArgs a) {
   griddep_wait();   // the workspace may still be read by an earlier product
   griddep_launch_dependents();
-  const int k32 = a.K >> 5;
-  const int64_t n = static_cast<int64_t>(a.N) * k32;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t row = i / k32;
-    const int k = static_cast<int>(i - row * k32) * 32;
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.codes) + row * (a.K >> 1) + (k >> 1));
-    const float s = __bfloat162float(static_cast<const __nv_bfloat16*>(a.scales)[row * (a.K / a.group) + k / a.group]);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * a.K + k);
+  const int64_t row = blockIdx.x;
+  const int n8 = a.K >> 3, g8 = __ffs(a.group >> 3) - 1;
+  const uint32_t* codes = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.codes) + row * (a.K >> 1));
+  const __nv_bfloat16* scales = static_cast<const __nv_bfloat16*>(a.scales) + row * (a.K / a.group);
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * a.K);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n8; i += 256) {
+    const uint32_t w = codes[i];
+    const float s = __bfloat162float(scales[i >> g8]);
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t r[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float v0 = static_cast<float>(static_cast<int>((w[j] >> (8 * q)) & 15u) - 8);
-        const float v1 = static_cast<float>(static_cast<int>((w[j] >> (8 * q + 4)) & 15u) - 8);
-        r[q] = pack_bf16x2(v0 * s, v1 * s);
-      }
-      dst[j] = make_uint4(r[0], r[1], r[2], r[3]);
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t p = w4_pair(w, q);      // 128 + code: exact, and so is the difference
+      v[q] = (__uint_as_float(p << 16) - 136.f) * s;
+      v[q + 4] = (__uint_as_float(p & 0xffff0000u) - 136.f) * s;
     }
+    dst[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
 }
 
@@ -481,12 +477,9 @@ cudaError_t launch_w4_mma(const W4Args& a, const W4Plan& p, cudaStream_t st) {
   }
 }
 
-cudaError_t launch_w4_expand(const W4ExpandArgs& a, int num_sms, cudaStream_t st) {
-  const int64_t n = static_cast<int64_t>(a.N) * (a.K / 32);
-  const int64_t want = (n + 255) / 256;
-  const int grid = static_cast<int>(want < 16LL * num_sms ? want : 16LL * num_sms);
+cudaError_t launch_w4_expand(const W4ExpandArgs& a, cudaStream_t st) {
   prof_begin(st, "w4_expand");
-  cudaError_t e = launch_pdl(w4_expand_kernel, dim3(grid), dim3(256), 0, st, 1, a);
+  cudaError_t e = launch_pdl(w4_expand_kernel, dim3(a.N), dim3(256), 0, st, 1, a);
   prof_end(st);
   return e;
 }
