@@ -129,6 +129,7 @@ struct GemmArgs {
   int32_t n_seg;
   int32_t T;
   int32_t K;
+  int32_t wrap_k;                // > 0 (swap orientation): the weights hold this K, read again for the activations beyond it
   // row_mode 2: per-group activations (swap orientation): the weight rows of
   //   group g = wrow / rows_per_group read activation rows g*act_group_stride + token.
   int32_t rows_per_group;

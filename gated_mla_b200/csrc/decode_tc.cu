@@ -805,6 +805,15 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), 1) decode_attn_
 //    bf16 [H, B, d_c] for the W_v product (a tensor-core GEMM with the gate in
 //    its epilogue). Block (0, 0) also clears that GEMM's split-K tickets.
 // ---------------------------------------------------------------------------
+// A merged latent value as `terms` bf16 terms, kDc apart. One term rounds it to 2^-8 relative; with two
+// (block scales) the W_v product reads it to 2^-16, and costs as much again as before (64
+// sequences, 32 heads: its K is 1024 instead of 512, over twice the CTAs).
+__device__ __forceinline__ void store_lat(__nv_bfloat16* dst, float v, int terms) {
+  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+  dst[0] = hi;
+  if (terms == 2) dst[kDc] = __float2bfloat16_rn(v - __bfloat162float(hi));
+}
+
 __global__ void __launch_bounds__(128) decode_merge_kernel(DecodeArgs a) {
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
@@ -823,8 +832,9 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(DecodeArgs a) {
           dst[j] = j == kDc ? -__int_as_float(0x7f800000) : 0.f;
         return;
       }
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.olat) + (static_cast<int64_t>(h) * a.B + b) * kDc;
-      for (int j = threadIdx.x; j < kDc; j += blockDim.x) dst[j] = __float2bfloat16_rn(0.f);
+      __nv_bfloat16* dst =
+      static_cast<__nv_bfloat16*>(a.olat) + (static_cast<int64_t>(h) * a.B + b) * (kDc * a.lat_terms);
+      for (int j = threadIdx.x; j < kDc * a.lat_terms; j += blockDim.x) dst[j] = __float2bfloat16_rn(0.f);
       return;
     }
   }
@@ -862,9 +872,10 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(DecodeArgs a) {
       dst[kDc + threadIdx.x] = threadIdx.x == 0 ? ((l > 0.f) ? mx + __log2f(l) : -__int_as_float(0x7f800000)) : 0.f;
     return;
   }
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.olat) + (static_cast<int64_t>(h) * a.B + b) * kDc;
+  __nv_bfloat16* dst =
+      static_cast<__nv_bfloat16*>(a.olat) + (static_cast<int64_t>(h) * a.B + b) * (kDc * a.lat_terms);
 #pragma unroll
-  for (int j = 0; j < kDc / 128; ++j) dst[j * 128 + threadIdx.x] = __float2bfloat16_rn(acc[j] * inv);
+  for (int j = 0; j < kDc / 128; ++j) store_lat(dst + j * 128 + threadIdx.x, acc[j] * inv, a.lat_terms);
 }
 
 // ---------------------------------------------------------------------------
@@ -899,9 +910,10 @@ __global__ void __launch_bounds__(128) decode_merge_ranks_kernel(MergeRanksArgs 
     mx = mn;
   }
   const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.olat) + (static_cast<int64_t>(h) * a.B + b) * kDc;
+  __nv_bfloat16* dst =
+      static_cast<__nv_bfloat16*>(a.olat) + (static_cast<int64_t>(h) * a.B + b) * (kDc * a.lat_terms);
 #pragma unroll
-  for (int j = 0; j < kDc / 128; ++j) dst[j * 128 + threadIdx.x] = __float2bfloat16_rn(acc[j] * inv);
+  for (int j = 0; j < kDc / 128; ++j) store_lat(dst + j * 128 + threadIdx.x, acc[j] * inv, a.lat_terms);
   if (a.gate_hard && threadIdx.x == 0)
     a.gvals[row] = head_gate(a.gate_logits + static_cast<int64_t>(b) * a.H, a.H, h, a.gate_mode, a.gate_topk);
 }
@@ -925,7 +937,8 @@ namespace gmla {
 // ---------------------------------------------------------------------------
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-DecodeLayout decode_layout(int B, int H, int eff_heads, int d_h, int d_c, int d_rope, int num_sms, bool fp8) {
+DecodeLayout decode_layout(int B, int H, int eff_heads, int d_h, int d_c, int d_rope, int num_sms, bool fp8,
+                           int lat_terms) {
   DecodeLayout L{};
   const int E = eff_heads;
   L.HG = E <= 16 ? 16 : (E % 64 == 0 ? 64 : (E % 32 == 0 ? 32 : 16));
@@ -954,9 +967,9 @@ DecodeLayout decode_layout(int B, int H, int eff_heads, int d_h, int d_c, int d_
   L.off_ctafirst = off;
   off = align256(off + static_cast<size_t>(L.G + 1) * 4);
   L.off_olat = off;
-  off = align256(off + static_cast<size_t>(H) * B * d_c * 2);
+  off = align256(off + static_cast<size_t>(H) * B * d_c * lat_terms * 2);
   L.off_gemm = off;
-  L.gemm_plan = gemm_swap_plan(H * d_h / 128, B, d_c, num_sms);
+  L.gemm_plan = gemm_swap_plan(H * d_h / 128, B, d_c * lat_terms, num_sms);
   off = align256(off + L.gemm_plan.ws_bytes);
   L.off_gvals = off;
   off = align256(off + static_cast<size_t>(B) * H * 4);

@@ -163,11 +163,12 @@ __global__ void __launch_bounds__(192, kSwap ? 1 : 2) gemm_bf16_tc_kernel(const 
       // Weight tiles are never written by a kernel: those of the first stages
       // are requested before waiting for the kernel that produces the activations.
       const int pre = min(num_kb, C::kStages);
+      auto wk = [&](int kb) { return (a.wrap_k && kb * 64 >= a.wrap_k) ? kb * 64 - a.wrap_k : kb * 64; };
       for (int kb = 0; kb < pre; ++kb) {
         uint8_t* sa = smem + kb * C::kStageBytes;
         mbar_arrive_expect_tx(&full[kb], C::kStageBytes);
         if (kSwap)
-          tma_load_2d(wmap, &full[kb], sa, (kb_begin + kb) * 64, tile.wrow0, pol_w);
+          tma_load_2d(wmap, &full[kb], sa, wk(kb_begin + kb), tile.wrow0, pol_w);
         else
           tma_load_2d(wmap, &full[kb], sa + C::kABytes, kb * 64, tile.wrow0, pol_w);
       }
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(192, kSwap ? 1 : 2) gemm_bf16_tc_kernel(const 
         uint8_t* sb = sa + C::kABytes;
         if (kb >= pre) mbar_arrive_expect_tx(&full[st], C::kStageBytes);
         if (kSwap) {
-          if (kb >= pre) tma_load_2d(wmap, &full[st], sa, (kb_begin + kb) * 64, tile.wrow0, pol_w);
+          if (kb >= pre) tma_load_2d(wmap, &full[st], sa, wk(kb_begin + kb), tile.wrow0, pol_w);
           tma_load_2d(&a.act, &full[st], sb, (kb_begin + kb) * 64, tile.act_row0, pol_x);
         } else {
           tma_load_2d(&a.act, &full[st], sa, kb * 64, tile.act_row0, pol_x);

@@ -186,6 +186,9 @@ CacheView cache_view(const gmla_config* c, const gmla_cache* k) {
   return v;
 }
 
+// bf16 terms of a merged latent value: see store_lat (decode_tc.cu)
+int lat_terms(const gmla_config* c) { return c->cache_dtype == GMLA_CACHE_FP8_BLOCK ? 2 : 1; }
+
 int gate_width(const gmla_config* c) {
   return c->gate_mode == GMLA_GATE_CHANNEL ? c->n_heads * c->d_h : c->n_heads;
 }
@@ -378,7 +381,7 @@ size_t gmla_decode_workspace_size(const gmla_config* cfg, int32_t B) {
   if (!cfg_valid(cfg) || B < 0) return 256;
   if (cfg->dtype == GMLA_FP32) return 256;
   return decode_layout(B, cfg->n_heads, decode_eff_heads(cfg), cfg->d_h, cfg->d_c, cfg->d_rope, num_sms(),
-                       fp8_cache(cfg)).total;
+                       fp8_cache(cfg), lat_terms(cfg)).total;
 }
 
 size_t gmla_prefill_workspace_size(const gmla_config* cfg, int32_t T, int32_t B) {
@@ -626,7 +629,7 @@ static gmla_status decode_impl(const gmla_config* cfg, const gmla_weights* w, co
   if (fp8 && (cfg->d_rope != 0 || cfg->d_c != 512))
     return fail(GMLA_ERR_UNSUPPORTED, "an FP8 cache covers NoPE decode with d_c = 512");
   const DecodeLayout L = decode_layout(B, cfg->n_heads, decode_eff_heads(cfg), cfg->d_h, cfg->d_c, cfg->d_rope,
-                                       num_sms(), fp8);
+                                       num_sms(), fp8, lat_terms(cfg));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeArgs a{};
   const int row = cfg->d_c + cfg->d_rope;
@@ -708,6 +711,7 @@ static gmla_status decode_impl(const gmla_config* cfg, const gmla_weights* w, co
   }
   a.qmul = reinterpret_cast<float*>(ws + L.off_qmul);
   a.olat = ws + L.off_olat;
+  a.lat_terms = lat_terms(cfg);
   const SwapPlan& sp = L.gemm_plan;
   a.gemm_counters = nullptr;
   a.n_gemm_tiles = 0;
@@ -716,8 +720,9 @@ static gmla_status decode_impl(const gmla_config* cfg, const gmla_weights* w, co
   const int HD = cfg->n_heads * cfg->d_h;
   const int G = gate_width(cfg);
   GemmArgs g{};
-  if (!make_tmap_2d(&g.act, a.olat, cfg->d_c, static_cast<uint64_t>(cfg->n_heads) * B,
-                    static_cast<uint64_t>(cfg->d_c) * 2, 64, sp.bn, true) ||
+  const int K = cfg->d_c * a.lat_terms;
+  if (!make_tmap_2d(&g.act, a.olat, K, static_cast<uint64_t>(cfg->n_heads) * B, static_cast<uint64_t>(K) * 2, 64, sp.bn,
+                    true) ||
       !make_tmap_2d(&g.wt[0], w->W_v, cfg->d_c, HD, static_cast<uint64_t>(cfg->d_c) * 2, 64, 128, true))
     return fail(GMLA_ERR_CUDA, "tensor maps for the W_v product failed");
   g.epi[0] = plain_seg(o_gated, HD, 1 << 30, 0, 0, false, nullptr, false, false);
@@ -731,7 +736,8 @@ static gmla_status decode_impl(const gmla_config* cfg, const gmla_weights* w, co
   g.seg_tile_begin[1] = HD / 128;
   g.n_seg = 1;
   g.T = B;
-  g.K = cfg->d_c;
+  g.K = K;
+  g.wrap_k = cfg->d_c;
   g.row_mode = 2;
   g.rows_per_group = cfg->d_h;
   g.act_group_stride = B;
@@ -762,7 +768,7 @@ gmla_status gmla_decode_partial(const gmla_config* cfg, const gmla_weights* w, c
 
 size_t gmla_decode_merge_workspace_size(const gmla_config* cfg, int32_t B) {
   if (!cfg_valid(cfg) || B < 0) return 256;
-  const size_t olat = align256(static_cast<size_t>(cfg->n_heads) * B * cfg->d_c * 2);
+  const size_t olat = align256(static_cast<size_t>(cfg->n_heads) * B * cfg->d_c * lat_terms(cfg) * 2);
   const size_t gv = align256(static_cast<size_t>(B) * cfg->n_heads * 4);
   return 256 + olat + gv;
 }
@@ -787,14 +793,16 @@ gmla_status gmla_decode_merge(const gmla_config* cfg, const gmla_weights* w, con
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int H = cfg->n_heads, HD = H * cfg->d_h, G = gate_width(cfg);
+  const int K = cfg->d_c * lat_terms(cfg);
   void* olat = ws + 256;
-  float* gvals = reinterpret_cast<float*>(ws + 256 + align256(static_cast<size_t>(H) * B * cfg->d_c * 2));
+  float* gvals = reinterpret_cast<float*>(ws + 256 + align256(static_cast<size_t>(H) * B * K * 2));
   MergeRanksArgs m{};
   m.partials = partials;
   m.R = R;
   m.B = B;
   m.H = H;
   m.olat = olat;
+  m.lat_terms = lat_terms(cfg);
   m.gate_logits = gate_logits;
   m.gate_mode = cfg->gate_mode;
   m.gate_topk = cfg->gate_topk;
@@ -803,10 +811,9 @@ gmla_status gmla_decode_merge(const gmla_config* cfg, const gmla_weights* w, con
   cudaError_t e = launch_decode_merge_ranks(m, st);
   if (e != cudaSuccess) return cuda_fail(e, "decode_merge");
   // o = gate ⊙ W_v^(h) O_lat^(h), the same tensor-core GEMM as gmla_decode's
-  const SwapPlan sp = gemm_swap_plan(HD / 128, B, cfg->d_c, num_sms());
+  const SwapPlan sp = gemm_swap_plan(HD / 128, B, K, num_sms());
   GemmArgs g{};
-  if (!make_tmap_2d(&g.act, olat, cfg->d_c, static_cast<uint64_t>(H) * B, static_cast<uint64_t>(cfg->d_c) * 2, 64,
-                    sp.bn, true) ||
+  if (!make_tmap_2d(&g.act, olat, K, static_cast<uint64_t>(H) * B, static_cast<uint64_t>(K) * 2, 64, sp.bn, true) ||
       !make_tmap_2d(&g.wt[0], w->W_v, cfg->d_c, HD, static_cast<uint64_t>(cfg->d_c) * 2, 64, 128, true))
     return fail(GMLA_ERR_CUDA, "tensor maps for the W_v product failed");
   g.epi[0] = plain_seg(o_gated, HD, 1 << 30, 0, 0, false, nullptr, false, false);
@@ -819,7 +826,8 @@ gmla_status gmla_decode_merge(const gmla_config* cfg, const gmla_weights* w, con
   g.seg_tile_begin[1] = HD / 128;
   g.n_seg = 1;
   g.T = B;
-  g.K = cfg->d_c;
+  g.K = K;
+  g.wrap_k = cfg->d_c;
   g.row_mode = 2;
   g.rows_per_group = cfg->d_h;
   g.act_group_stride = B;

@@ -78,7 +78,8 @@ struct DecodeArgs {
   int4* seg_info;            // workspace: [max_seg] {sequence, first tile, end tile, length}
   int32_t* seq_first_seg;    // workspace: [B + 1]
   int32_t* cta_first_seg;    // workspace: [G + 1]
-  void* olat;                // workspace: [H, B, d_c] bf16 merged latent outputs
+  void* olat;                // workspace: [H, B, lat_terms, d_c] bf16 merged latent outputs
+  int32_t lat_terms;         // 2 (block scales): a second bf16 term holds what the first leaves, else 1
   int32_t* gemm_counters;    // workspace: split-K tickets of the W_v GEMM
   int32_t n_gemm_tiles;
   int* status;
@@ -113,7 +114,8 @@ struct DecodeArgs {
 struct MergeRanksArgs {
   const float* partials;     // [R, B, H, d_c + 4]
   int32_t R, B, H;
-  void* olat;                // [H, B, d_c] bf16
+  void* olat;                // [H, B, lat_terms, d_c] bf16
+  int32_t lat_terms;
   const float* gate_logits;  // [B, H] (hard gates only) or null
   int32_t gate_mode, gate_topk, gate_hard;
   float* gvals;              // [B, H]
@@ -125,11 +127,12 @@ struct DecodeLayout {
   size_t off_qa, off_opart, off_ml, off_seg, off_seqfirst, off_ctafirst, off_olat, off_gemm;
   size_t off_gvals, off_hslot, off_nact, off_qmul, total;
   int HG, n_hg, G, max_seg;
-  SwapPlan gemm_plan;        // the W_v GEMM (heads x 128 rows, B tokens, K = d_c)
+  SwapPlan gemm_plan;        // the W_v GEMM (heads x 128 rows, B tokens, K = lat_terms d_c)
 };
 // eff_heads: the most heads a sequence attends with (H, or k with top-k gates),
 // which sets the head groups of the attention kernel.
-DecodeLayout decode_layout(int B, int H, int eff_heads, int d_h, int d_c, int d_rope, int num_sms, bool fp8 = false);
+DecodeLayout decode_layout(int B, int H, int eff_heads, int d_h, int d_c, int d_rope, int num_sms, bool fp8 = false,
+                           int lat_terms = 1);
 // sequences per CTA of the tensor-core absorb (N of its MMA)
 int absorb_tile_n(int B);
 cudaError_t launch_decode_bf16(DecodeArgs& a, cudaStream_t st);
