@@ -969,7 +969,7 @@ DecodeLayout decode_layout(int B, int H, int eff_heads, int d_h, int d_c, int d_
   L.off_olat = off;
   off = align256(off + static_cast<size_t>(H) * B * d_c * lat_terms * 2);
   L.off_gemm = off;
-  L.gemm_plan = gemm_swap_plan(H * d_h / 128, B, d_c * lat_terms, num_sms);
+  L.gemm_plan = gemm_swap_plan(H * d_h / 128, B, d_c * lat_terms, num_sms, lat_terms == 2);
   off = align256(off + L.gemm_plan.ws_bytes);
   L.off_gvals = off;
   off = align256(off + static_cast<size_t>(B) * H * 4);

@@ -526,9 +526,13 @@ int gemm_weight_tile(bool swap, int bn) { return swap ? 128 : bn; }
 
 int gemm_swap_bn(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : T <= 128 ? 128 : 256; }
 
-SwapPlan gemm_swap_plan(int wtiles, int T, int K, int num_sms) {
+SwapPlan gemm_swap_plan(int wtiles, int T, int K, int num_sms, bool split_tokens) {
   SwapPlan p{};
   p.bn = gemm_swap_bn(T);
+  // split_tokens (a weight that L2 holds, read by every token tile): narrower token tiles before K splits, as
+  // long as the tiles fit one CTA per SM (W_v of 32 heads, 64 sequences, K = 1024: 13.1 us against 17.2)
+  if (split_tokens)
+    while (p.bn > 16 && wtiles * ((2 * T + p.bn - 1) / p.bn) <= num_sms) p.bn /= 2;
   p.ttiles = (T + p.bn - 1) / p.bn;
   const int tiles = wtiles * p.ttiles;
   const int num_kb = (K + 63) / 64;

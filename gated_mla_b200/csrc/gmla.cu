@@ -811,7 +811,7 @@ gmla_status gmla_decode_merge(const gmla_config* cfg, const gmla_weights* w, con
   cudaError_t e = launch_decode_merge_ranks(m, st);
   if (e != cudaSuccess) return cuda_fail(e, "decode_merge");
   // o = gate ⊙ W_v^(h) O_lat^(h), the same tensor-core GEMM as gmla_decode's
-  const SwapPlan sp = gemm_swap_plan(HD / 128, B, K, num_sms());
+  const SwapPlan sp = gemm_swap_plan(HD / 128, B, K, num_sms(), m.lat_terms == 2);
   GemmArgs g{};
   if (!make_tmap_2d(&g.act, olat, K, static_cast<uint64_t>(H) * B, static_cast<uint64_t>(K) * 2, 64, sp.bn, true) ||
       !make_tmap_2d(&g.wt[0], w->W_v, cfg->d_c, HD, static_cast<uint64_t>(cfg->d_c) * 2, 64, 128, true))

@@ -56,7 +56,7 @@ struct SwapPlan {
   int bn, ttiles, tiles, splits, kb_per_split;
   size_t ws_bytes;
 };
-SwapPlan gemm_swap_plan(int wtiles, int T, int K, int num_sms);
+SwapPlan gemm_swap_plan(int wtiles, int T, int K, int num_sms, bool split_tokens = false);
 
 // ----- decode (decode_tc.cu) -----
 struct DecodeArgs {
