@@ -147,6 +147,10 @@ struct GemmArgs {
   int32_t tiles_per_seq;
   int32_t act_seq_stride;
   int32_t weights_written;       // 1: the weights were written by an earlier kernel of the stream
+  // many tokens: operands in fp16 whose rows are scaled; output (t, f) is multiplied by t_scale[t] f_scale[f]
+  int32_t f16;
+  const float* t_scale;
+  const float* f_scale;          // readable up to a whole weight tile
   const int32_t* cu_seqlens;
   const int32_t* positions;
   const int32_t* seq_ids;

@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(192, kSwap ? 1 : 2) gemm_bf16_tc_kernel(const 
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, BN, false, false);
+      constexpr uint32_t kDescBf16 = idesc_bf16_f32(128, BN, false, false);
+      const uint32_t idesc = !kSwap && a.f16 ? idesc_f16(kDescBf16) : kDescBf16;
       bool ok = true;
       for (int kb = 0; kb < num_kb; ++kb) {
         const int st = kb % C::kStages;
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(192, kSwap ? 1 : 2) gemm_bf16_tc_kernel(const 
         const int tok = tile.tok0 + r;
         int pos = 0;
         int64_t row = tok;
+        const float t_scale = a.f16 && tok_ok ? a.t_scale[tok] : 1.f;
         if (tok_ok && (e.rope || e.cache_scatter)) pos = a.positions[tok];
         if (tok_ok && e.cache_scatter) {
           row = cache_row(a.cache, a.seq_ids[tok], pos);
@@ -344,6 +346,16 @@ __global__ void __launch_bounds__(192, kSwap ? 1 : 2) gemm_bf16_tc_kernel(const 
           float x[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(v[j]);
+          if (a.f16) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+              const float4 s = *reinterpret_cast<const float4*>(a.f_scale + f0 + j);
+              x[j] = x[j] * t_scale * s.x;
+              x[j + 1] = x[j + 1] * t_scale * s.y;
+              x[j + 2] = x[j + 2] * t_scale * s.z;
+              x[j + 3] = x[j + 3] * t_scale * s.w;
+            }
+          }
           if (e.rope) {
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {

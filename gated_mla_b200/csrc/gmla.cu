@@ -962,10 +962,10 @@ gmla_status gmla_prefill(const gmla_config* cfg, const gmla_weights* w, const vo
 }
 
 // ---------------------------------------------------------------------------
-// y [T, d_model] = src [T, H*d_h] W^T on the tensor-core GEMM (bf16). weights_written: W
-// comes from an earlier kernel of the stream.
-static gmla_status out_gemm(const gmla_config* cfg, const void* src, int T, const void* W, bool weights_written,
-                            void* y, int* status, cudaStream_t st, const char* name) {
+// y [T, d_model] = src [T, H*d_h] W^T on the tensor-core GEMM (bf16). With scales (more than 256
+// tokens) W and src come from earlier kernels of the stream, as fp16 rows to be scaled.
+static gmla_status out_gemm(const gmla_config* cfg, const void* src, int T, const void* W, const float* t_scale,
+                            const float* f_scale, void* y, int* status, cudaStream_t st, const char* name) {
   const int HD = cfg->n_heads * cfg->d_h, dm = cfg->d_model;
   if (HD % 8) return fail(GMLA_ERR_UNSUPPORTED, "bf16 path needs H*d_h %% 8 == 0");
   GemmArgs a{};
@@ -984,7 +984,10 @@ static gmla_status out_gemm(const gmla_config* cfg, const void* src, int T, cons
   a.T = T;
   a.K = HD;
   a.row_mode = 0;
-  a.weights_written = weights_written ? 1 : 0;
+  a.weights_written = f_scale ? 1 : 0;
+  a.f16 = f_scale ? 1 : 0;
+  a.t_scale = t_scale;
+  a.f_scale = f_scale;
   a.status = status;
   const int ttiles = swap ? sp.ttiles : (T + 127) / 128;
   if (swap) {
@@ -1036,16 +1039,17 @@ gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w, const v
     cudaError_t e = launch_gemm_f32(a, st);
     return e == cudaSuccess ? GMLA_OK : cuda_fail(e, "gate_out (fp32)");
   }
-  return out_gemm(cfg, src, T, w->W_o, false, y, status, st, "gate_out");
+  return out_gemm(cfg, src, T, w->W_o, nullptr, nullptr, y, status, st, "gate_out");
 }
 
 // ---------------------------------------------------------------------------
 constexpr int kW4MaxK = 1 << 24;
 
 // workspace: status word; few tokens: the activations in the order the kernel reads them, with
-// their group sums; many: gate ⊙ o [T, K] bf16, then W expanded to bf16 [N, K]
+// their group sums; many: gate ⊙ o [T, K] and W [N, K] in fp16, the scales of their rows
 static size_t w4_act_bytes(const W4Plan& p) {
-  return align256(static_cast<size_t>(p.T8) * (p.K256 * 2 + (p.K256 / kW4Chunk + 1) * 32));
+  return p.nt ? align256(static_cast<size_t>(p.T8) * (p.K256 * 2 + p.K256 / kW4Chunk * 32))
+              : align256(static_cast<size_t>(p.T8) * p.K256 * 2) + align256(static_cast<size_t>(p.T8) * 4);
 }
 
 size_t gmla_gate_out_w4_workspace_size(const gmla_config* cfg, int32_t T) {
@@ -1053,7 +1057,8 @@ size_t gmla_gate_out_w4_workspace_size(const gmla_config* cfg, int32_t T) {
   const size_t HD = static_cast<size_t>(cfg->n_heads) * cfg->d_h;
   if (T == 0 || HD > kW4MaxK) return 256;
   const W4Plan p = w4_plan(cfg->d_model, T, static_cast<int>(HD), num_sms());
-  return 256 + w4_act_bytes(p) + (p.nt ? 0 : align256(static_cast<size_t>(cfg->d_model) * HD * 2));
+  const size_t N = static_cast<size_t>(cfg->d_model);
+  return 256 + w4_act_bytes(p) + (p.nt ? 0 : align256(N * HD * 2) + align256((N + 255) / 256 * 1024));
 }
 
 gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const void* o, int32_t T,
@@ -1083,17 +1088,22 @@ gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const vo
   int* status = static_cast<int*>(workspace);
   uint8_t* act = static_cast<uint8_t*>(workspace) + 256;
   const W4Plan plan = w4_plan(N, T, K, sms);
-  uint8_t* rest = act + w4_act_bytes(plan);
-  const W4PrepArgs p{o,        gate_logits,    act,            T,         K,       cfg->n_heads,
-                     cfg->d_h, cfg->gate_mode, cfg->gate_topk, w4->group, plan.T8, plan.K256, plan.nt};
-  cudaError_t e = plan.nt || gate_logits ? launch_w4_prep(p, sms, st) : cudaSuccess;
-  if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4");
+  W4PrepArgs p{o,        gate_logits,    act,            T,         K,       cfg->n_heads,
+               cfg->d_h, cfg->gate_mode, cfg->gate_topk, w4->group, plan.T8, plan.K256, plan.nt, nullptr};
+  cudaError_t e;
   if (!plan.nt) {
-    const W4ExpandArgs x{w4->codes, w4->scales, rest, N, K, w4->group};
+    uint8_t* W = act + w4_act_bytes(plan);
+    p.t_scale = reinterpret_cast<float*>(act + align256(static_cast<size_t>(T) * K * 2));
+    float* f_scale = reinterpret_cast<float*>(W + align256(static_cast<size_t>(N) * K * 2));
+    e = launch_w4_wide_prep(p, st);
+    if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4");
+    const W4ExpandArgs x{w4->codes, w4->scales, W, f_scale, N, K, w4->group};
     e = launch_w4_expand(x, st);
     if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4: expand");
-    return out_gemm(cfg, gate_logits ? act : o, T, rest, true, y, status, st, "gate_out_w4");
+    return out_gemm(cfg, act, T, W, p.t_scale, f_scale, y, status, st, "gate_out_w4");
   }
+  e = launch_w4_prep(p, sms, st);
+  if (e != cudaSuccess) return cuda_fail(e, "gate_out_w4");
   W4Args a{};
   if (!make_tmap_2d_u8(&a.wmap, w4->codes, K / 2, N, K / 2, 128, 128))
     return fail(GMLA_ERR_CUDA, "tensor map for gate_out_w4 failed");

@@ -246,6 +246,7 @@ struct W4PrepArgs {
   void* out;                 // in the order the product reads (w4.cu)
   int32_t T, K, H, d_h, gate_mode, gate_topk, group;
   int32_t T8, K256, nt;      // of the plan
+  float* t_scale;            // many tokens: [T], what a token's sums are multiplied by
 };
 struct W4Args {
   CUtensorMap wmap;          // 2D [N, K / 2] bytes
@@ -259,7 +260,8 @@ struct W4Args {
 struct W4ExpandArgs {
   const void* codes;
   const void* scales;
-  void* out;                 // [N, K] bf16
+  void* out;                 // [N, K] fp16
+  float* f_scale;            // [N], what a row's sums are multiplied by
   int32_t N, K, group;
 };
 struct W4Plan {
@@ -270,6 +272,7 @@ constexpr int kW4MaxMma = 256;
 W4Plan w4_plan(int N, int T, int K, int num_sms);
 cudaError_t launch_w4_prep(const W4PrepArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_w4_mma(const W4Args& a, const W4Plan& p, cudaStream_t st);
+cudaError_t launch_w4_wide_prep(const W4PrepArgs& a, cudaStream_t st);
 cudaError_t launch_w4_expand(const W4ExpandArgs& a, cudaStream_t st);
 
 // ----- elementwise helpers (gmla.cu) -----

@@ -444,6 +444,9 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_ma
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
+// The same with A and B in fp16 (format code 0).
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t idesc_bf16) { return idesc_bf16 & ~((7u << 7) | (7u << 10)); }
+
 // Instruction descriptor of kind::f8f6f4 with E4M3 A/B (format code 0) and fp32 D.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4)                                   // D format: f32

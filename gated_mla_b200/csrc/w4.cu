@@ -23,9 +23,15 @@
 // K is split over the CTAs of a cluster, which add their fp32 partial tiles
 // through distributed shared memory in a fixed order.
 //
-// Many tokens (above 256): the codes expand once to bf16 in the workspace (w4_expand), which rounds
-// (code - 8) * scale to half a step, 2^-8 relative, as a bf16 weight is; then the tcgen05 GEMM of
-// the bf16 path runs.
+// Many tokens (above 256): the codes expand once to fp16 in the workspace (w4_expand), the gated
+// activations are stored as fp16 too (w4_wide_prep), and the tcgen05 GEMM of the bf16 path runs on
+// them. A code times a scale has 3 + 8 significant bits, fp16's 11, so no weight is rounded (in bf16
+// each would be, by 2^-8: at 2000 tokens, 7168 x 8192, an error of 0.0027 instead of 0.0017, nearly
+// all of it the result's own rounding). What fp16 lacks is range, so each weight row and each token
+// row is first multiplied by a power of two that brings its largest element near fp16's top; the
+// GEMM's epilogue takes both back. Elements down to 2^-28 of the largest keep their full precision.
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -100,52 +106,52 @@ struct W4Cfg {
 
 }  // namespace
 
+// 8 consecutive elements of gate ⊙ o, in fp32
+__device__ __forceinline__ void w4_gated8(const W4PrepArgs& a, int t, int k, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + static_cast<int64_t>(t) * a.K + k);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  }
+  if (!a.gate_logits) return;
+  if (a.gate_mode == kGateChannel) {
+    const float4* z = reinterpret_cast<const float4*>(a.gate_logits + static_cast<int64_t>(t) * a.K + k);
+    const float4 z0 = z[0], z1 = z[1];
+    const float zz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= 1.f / (1.f + expf(-zz[j]));
+  } else {   // d_h is a multiple of 8: one head for the run
+    const float gv = head_gate(a.gate_logits + static_cast<int64_t>(t) * a.H, a.H, k / a.d_h, a.gate_mode, a.gate_topk);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= gv;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // a = gate ⊙ o in bf16, in fragment order, and -136 times its sum over each group.
-// out: for each token tile of 8 nt and each chunk of 256 k, [8 steps][nt][g * 4 + c][8 bf16]: token 8 n + g of the tile, k = 32 step + 8 c +
-// (0 4 1 5 2 6 3 7), then the sums [256 / group][8 nt] fp32 in 256 nt bytes. Tokens and k behind
-// the end are zeros. A thread makes one run of 8 k; the runs of a group are neighbouring
-// lanes. nt = 0 (for the GEMM): out is [T, K] as it is, and no sums are made.
+// out: for each token tile of 8 nt and each chunk of 256 k, [8 steps][nt][g * 4 + c][8 bf16]: token 8 n + g of the
+// tile, k = 32 step + 8 c + (0 4 1 5 2 6 3 7), then the sums [256 / group][8 nt] fp32 in 256 nt bytes.
+// Tokens and k behind the end are zeros. A thread makes one run of 8 k; the runs of a group are
+// neighbouring lanes.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
   griddep_wait();
   griddep_launch_dependents();   // all earlier kernels are done: the product may begin to load its weights
   const int k8 = a.K256 >> 3;
-  const int64_t n = static_cast<int64_t>(a.T8) * k8;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const uint32_t n = static_cast<uint32_t>(a.T8) * k8;      // at most 256 tokens, 2^21 runs each
   const int g8 = a.group >> 3;
-  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x; i0 < n; i0 += stride) {   // uniform over a block
-    const int64_t i = i0 + threadIdx.x;
-    const int t = n >> 32 ? static_cast<int>(i / k8) : static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(k8));
-    const int k = static_cast<int>(i - static_cast<int64_t>(t) * k8) * 8;
+  for (uint32_t i0 = blockIdx.x * blockDim.x; i0 < n; i0 += gridDim.x * blockDim.x) {   // uniform over a block
+    const uint32_t i = i0 + threadIdx.x;
+    const int t = static_cast<int>(i / k8);
+    const int k = static_cast<int>(i - static_cast<uint32_t>(t) * k8) * 8;
     uint32_t w[4] = {0, 0, 0, 0};
-    const bool live = i < n && t < a.T && k < a.K;
-    if (live) {
-      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) +
-                                                      static_cast<int64_t>(t) * a.K + k);
-      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-      if (a.gate_logits) {
-        float g[8];
-        if (a.gate_mode == kGateChannel) {
-          const float4* z = reinterpret_cast<const float4*>(a.gate_logits + static_cast<int64_t>(t) * a.K + k);
-          const float4 z0 = z[0], z1 = z[1];
-          const float zz[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
+    if (i < n && t < a.T && k < a.K) {
+      float v[8];
+      w4_gated8(a, t, k, v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = 1.f / (1.f + expf(-zz[j]));
-        } else {   // d_h is a multiple of 8: one head for the run
-          const float gv = head_gate(a.gate_logits + static_cast<int64_t>(t) * a.H, a.H, k / a.d_h, a.gate_mode,
-                                     a.gate_topk);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) g[j] = gv;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = pack_bf16x2(__uint_as_float(w[j] << 16) * g[2 * j], __uint_as_float(w[j] & 0xffff0000u) * g[2 * j + 1]);
-      }
-    }
-    if (a.nt == 0) {
-      if (i < n) reinterpret_cast<uint4*>(a.out)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-      continue;
+      for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
     }
     uint4 r;
     r.x = __byte_perm(w[0], w[2], 0x5410);
@@ -380,20 +386,91 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
 }
 
 // ---------------------------------------------------------------------------
-// bf16((code - 8) * scale), 8 codes a thread, one row a block: bound by the bytes that it writes
+// Many tokens: one row of fp16 operands a block, and the power of two that its sums are
+// multiplied by afterwards. Bound by the bytes that they read and write.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }   // -126 .. 127
+
+// The largest of the block's values (s_top: a word a warp).
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s_top) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = v;
+  __syncthreads();
+  uint32_t top = 0;
+  for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) top = max(top, s_top[i]);
+  return top;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+constexpr int kWideThreads = 512, kWideVec = 4;   // 16384 k in registers between the maximum and the rounding
+
+__global__ void __launch_bounds__(kWideThreads) w4_wide_prep_kernel(W4PrepArgs a) {
+  __shared__ uint32_t s_top[kWideThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t = blockIdx.x, n8 = a.K >> 3;
+  float v[kWideVec][8];
+  uint32_t top = 0;      // magnitudes compare as their bits do
+#pragma unroll
+  for (int i = 0; i < kWideVec; ++i) {
+    const int k8 = threadIdx.x + i * kWideThreads;
+    if (k8 >= n8) break;
+    w4_gated8(a, t, k8 * 8, v[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
+  }
+  for (int k8 = threadIdx.x + kWideVec * kWideThreads; k8 < n8; k8 += kWideThreads) {
+    float u[8];
+    w4_gated8(a, t, k8 * 8, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(u[j]) & 0x7fffffffu);
+  }
+  top = block_max(top, s_top);
+  const int e = max(-110, min(127, static_cast<int>(top >> 23) - 127));   // 2^e <= largest < 2^(e + 1); infinities and NaN: 127
+  const float mul = pow2(14 - e);
+  if (threadIdx.x == 0) a.t_scale[t] = pow2(e - 14);
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + static_cast<int64_t>(t) * a.K);
+  auto store = [&](int k8, const float (&u)[8]) {
+    dst[k8] = make_uint4(pack_f16x2(u[0] * mul, u[1] * mul), pack_f16x2(u[2] * mul, u[3] * mul),
+                         pack_f16x2(u[4] * mul, u[5] * mul), pack_f16x2(u[6] * mul, u[7] * mul));
+  };
+#pragma unroll
+  for (int i = 0; i < kWideVec; ++i) {
+    const int k8 = threadIdx.x + i * kWideThreads;
+    if (k8 >= n8) break;
+    store(k8, v[i]);
+  }
+  for (int k8 = threadIdx.x + kWideVec * kWideThreads; k8 < n8; k8 += kWideThreads) {
+    float u[8];
+    w4_gated8(a, t, k8 * 8, u);
+    store(k8, u);
+  }
+}
+
 __global__ void __launch_bounds__(256) w4_expand_kernel(W4ExpandArgs a) {
+  __shared__ uint32_t s_top[8];
   griddep_wait();   // the workspace may still be read by an earlier product
   griddep_launch_dependents();
   const int64_t row = blockIdx.x;
-  const int n8 = a.K >> 3, g8 = __ffs(a.group >> 3) - 1;
+  const int n8 = a.K >> 3, g8 = __ffs(a.group >> 3) - 1, n_groups = a.K / a.group;
   const uint32_t* codes = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.codes) + row * (a.K >> 1));
-  const __nv_bfloat16* scales = static_cast<const __nv_bfloat16*>(a.scales) + row * (a.K / a.group);
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * a.K);
+  const uint16_t* scales = static_cast<const uint16_t*>(a.scales) + row * n_groups;
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + row * a.K);
+  uint32_t top = 0;
+  for (int i = threadIdx.x; i < n_groups; i += 256) top = max(top, scales[i] & 0x7fffu);
+  top = block_max(top, s_top);
+  // the largest scale to 2^11 .. 2^12: 8 of it stay below 2^15
+  const int e = max(-100, min(127, static_cast<int>(top >> 7) - 127));
+  const float mul = pow2(11 - e);
+  if (threadIdx.x == 0) a.f_scale[row] = pow2(e - 11);
 #pragma unroll 4
   for (int i = threadIdx.x; i < n8; i += 256) {
     const uint32_t w = codes[i];
-    const float s = __bfloat162float(scales[i >> g8]);
+    const float s = __uint_as_float(static_cast<uint32_t>(scales[i >> g8]) << 16) * mul;
     float v[8];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -401,7 +478,7 @@ __global__ void __launch_bounds__(256) w4_expand_kernel(W4ExpandArgs a) {
       v[q] = (__uint_as_float(p << 16) - 136.f) * s;
       v[q + 4] = (__uint_as_float(p & 0xffff0000u) - 136.f) * s;
     }
-    dst[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    dst[i] = make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
   }
 }
 
@@ -465,6 +542,13 @@ cudaError_t launch_w4_prep(const W4PrepArgs& a, int num_sms, cudaStream_t st) {
   const int grid = static_cast<int>(want < 8LL * num_sms ? want : 8LL * num_sms);
   prof_begin(st, "w4_prep");
   cudaError_t e = launch_pdl(w4_prep_kernel, dim3(grid), dim3(256), 0, st, 1, a);
+  prof_end(st);
+  return e;
+}
+
+cudaError_t launch_w4_wide_prep(const W4PrepArgs& a, cudaStream_t st) {
+  prof_begin(st, "w4_wide_prep");
+  cudaError_t e = launch_pdl(w4_wide_prep_kernel, dim3(a.T), dim3(kWideThreads), 0, st, 1, a);
   prof_end(st);
   return e;
 }

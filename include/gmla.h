@@ -262,8 +262,9 @@ GMLA_API gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w
  *   workspace    gmla_gate_out_w4_workspace_size(cfg, T) bytes; calls that may
  *                overlap need workspaces of their own
  * Up to 256 tokens the codes are multiplied as they are and the scale is applied in
- * fp32: no weight is rounded. Above that the weights are expanded to bf16 in the
- * workspace once a call (each rounded once, as a bf16 weight is).
+ * fp32: no weight is rounded. Above that weights and activations become fp16 numbers
+ * under a power of two for each row, in the workspace: weights exact while the scales
+ * of a row lie within 2^28 of one another, activations rounded to 2^-12.
  * ------------------------------------------------------------------------- */
 GMLA_API gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4,
                                       const void* o, int32_t T, const float* gate_logits,
