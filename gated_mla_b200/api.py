@@ -150,7 +150,8 @@ def plan_batch(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     gets the entries of the pages that new rows begin, taken from ``free_pages`` in the
     order of the sequences. ``n_tokens`` is the number of token rows, at least the sum of
     new_lens; rows behind the last sequence get -1. ``out`` reuses the buffers of an
-    earlier plan of the same sizes. A batch that does not fit is planned as empty and
+    earlier plan of the same sizes (copy its ``seq_lens`` first when they are this
+    step's ``cached_lens``). A batch that does not fit is planned as empty and
     reported by ``sync_status``.
     """
     dev, B, T = cached_lens.device, cached_lens.shape[0], n_tokens

@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(256) cache_append_kernel(AppendArgs a) {
   if (w == 0 && t < a.T)
     prefetch_l2(static_cast<const __nv_bfloat16*>(a.latents) + static_cast<int64_t>(t) * a.stride + lane * 16);
   const int total = min(cu_end, a.T);
+  if (cu_end > a.T && blockIdx.x == 0 && threadIdx.x == 0) report_status(a.status, kStatusRange);
   const int t_end = min(t + a.window, total);
   if (t >= t_end || t < cu_0) return;   // uniform over the unit
   int b = t >= cu_g && t < cu_g1 ? guess : find_seq(a.cu, a.B, t, lane);

@@ -1137,6 +1137,7 @@ gmla_status gmla_plan_batch(const int32_t* cached_lens, const int32_t* new_lens,
     return fail(GMLA_ERR_INVALID_ARG, "page_size and max_pages_per_seq must be > 0");
   if (static_cast<int64_t>(page_size) * max_pages_per_seq > (int64_t(1) << 31) - 1)
     return fail(GMLA_ERR_UNSUPPORTED, "a sequence of more than 2^31 - 1 rows");
+  if (T > 1 << 30) return fail(GMLA_ERR_UNSUPPORTED, "plan_batch covers T <= 2^30");
   GMLA_TRY(check_status_workspace(workspace, workspace_bytes, "plan_batch"));
   GMLA_TRY(check_words(cached_lens, "cached_lens", B > 0));
   GMLA_TRY(check_words(new_lens, "new_lens", B > 0));
@@ -1148,6 +1149,11 @@ gmla_status gmla_plan_batch(const int32_t* cached_lens, const int32_t* new_lens,
   GMLA_TRY(check_ptr(seq_ids, "seq_ids", T > 0));
   GMLA_TRY(check_ptr(slots, "slots", T > 0));
   GMLA_TRY(check_ptr(pages_used, "pages_used"));
+  // every block reads the request lengths while the first one writes
+  const auto overlap = [](const int32_t* x, int64_t nx, const int32_t* y, int64_t ny) { return x < y + ny && y < x + nx; };
+  for (const int32_t* in : {cached_lens, new_lens})
+    if (overlap(in, B, seq_lens, B) || overlap(in, B, cu_seqlens, int64_t(B) + 1))
+      return fail(GMLA_ERR_INVALID_ARG, "seq_lens and cu_seqlens must not overlap cached_lens or new_lens");
   PlanArgs a{};
   a.cached = cached_lens;
   a.fresh = new_lens;
@@ -1184,6 +1190,7 @@ gmla_status gmla_add_rms_norm(int32_t dtype, const void* x, int64_t x_stride, co
   if ((group != 0) != (codes != nullptr) || (group != 0) != (scales != nullptr))
     return fail(GMLA_ERR_INVALID_ARG, "codes and scales go with a group > 0");
   if (!out && !residual_out && !codes) return fail(GMLA_ERR_INVALID_ARG, "no output is given");
+  if (out && out == residual_out) return fail(GMLA_ERR_INVALID_ARG, "out and residual_out are the same rows");
   GMLA_TRY(check_ptr(x, "x"));
   GMLA_TRY(check_ptr(residual, "residual", false));
   GMLA_TRY(check_ptr(weight, "weight", false));

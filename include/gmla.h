@@ -285,6 +285,7 @@ GMLA_API size_t gmla_gate_out_w4_workspace_size(const gmla_config* cfg, int32_t 
  *                a sequence's new rows begin are written, all others are left as they were
  *   T            token rows of the outputs (>= the sum of new_lens)
  *   seq_lens     [B] = cached + new;  cu_seqlens [B+1] = prefix sums of new_lens
+ *                (neither may overlap cached_lens or new_lens: copy seq_lens for the next step)
  *   positions, seq_ids [T] int32, slots [T] int64: packed by sequence; slot = page *
  *                page_size + row. Rows behind the last sequence's get -1 in all three
  *   pages_used   [1] int32
@@ -336,7 +337,7 @@ GMLA_API gmla_status gmla_add_rms_norm(int32_t dtype, const void* x, int64_t x_s
  * scale and that one; when it grows, the held codes are rounded again to the new
  * scale. Rows of other blocks, and rows behind the new ones, are left as they were.
  * Sequences must not share the pages that they write. A length or page out of range
- * sets GMLA_ERR_DEVICE_RANGE and its rows are skipped.
+ * sets GMLA_ERR_DEVICE_RANGE and its rows are skipped; cu_seqlens[B] > T sets it too.
  *   workspace    256 bytes (the status word)
  * ------------------------------------------------------------------------- */
 GMLA_API gmla_status gmla_cache_append(const gmla_config* cfg, const gmla_cache* cache,

@@ -171,6 +171,18 @@ def test_append_out_of_range_is_skipped_and_reported():
         assert torch.equal(changed, want), what
 
 
+def test_append_of_fewer_rows_than_the_offsets_name_is_reported():
+    import gated_mla_b200 as gmla
+    model = _model()
+    pool = Pool(2, 64, 16, 16)
+    x = _latents(6, 1)
+    model.cache_append(x, torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda"),
+                       torch.tensor([4, 5], dtype=torch.int32, device="cuda"), pool.cache)
+    with pytest.raises(gmla._lib.GmlaError) as e:
+        model.sync_status()
+    assert e.value.status == gmla._lib.GMLA_ERR_DEVICE_RANGE
+
+
 # ---------------------------------------------------------------------------
 def _attend(H, lens, page, block, gate="channel", seed=0, q_mul=1.0, spread=1.0, d_h=128, cap=None, plant=None, topk=0,
             seqs=None, logits=True):

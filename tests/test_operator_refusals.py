@@ -32,8 +32,8 @@ def _cache(L, **kw):
 
 
 def _plan(L, **kw):
-    a = dict(cached_lens=P, new_lens=P, B=2, free_pages=P, n_free=4, page_size=16, block_table=P, max_pages_per_seq=4, T=8,
-             seq_lens=P, cu_seqlens=P, positions=P, seq_ids=P, slots=P, pages_used=P, ws=P, ws_bytes=256, stream=None)
+    a = dict(cached_lens=P, new_lens=P + 256, B=2, free_pages=P, n_free=4, page_size=16, block_table=P, max_pages_per_seq=4, T=8,
+             seq_lens=P + 512, cu_seqlens=P + 768, positions=P, seq_ids=P, slots=P, pages_used=P, ws=P, ws_bytes=256, stream=None)
     a.update(kw)
     return L.gmla_plan_batch(*a.values())
 
@@ -42,7 +42,8 @@ def _plan(L, **kw):
                                  dict(cached_lens=None), dict(new_lens=None), dict(free_pages=None), dict(block_table=None),
                                  dict(seq_lens=None), dict(cu_seqlens=None), dict(positions=P + 4), dict(slots=P + 8),
                                  dict(seq_ids=None), dict(pages_used=None), dict(cached_lens=P + 1), dict(new_lens=P + 2),
-                                 dict(free_pages=P + 2)])
+                                 dict(free_pages=P + 2), dict(seq_lens=P), dict(seq_lens=P + 256), dict(cu_seqlens=P),
+                                 dict(cu_seqlens=P + 256), dict(cached_lens=P + 516), dict(new_lens=P + 776)])
 def test_plan_batch(L, bad):
     assert _plan(L, **bad) == L.GMLA_ERR_INVALID_ARG
 
@@ -51,10 +52,11 @@ def test_plan_batch_workspace_and_range(L):
     assert _plan(L, ws=None) == L.GMLA_ERR_WORKSPACE
     assert _plan(L, ws_bytes=255) == L.GMLA_ERR_WORKSPACE
     assert _plan(L, page_size=1 << 20, max_pages_per_seq=1 << 12) == L.GMLA_ERR_UNSUPPORTED
+    assert _plan(L, T=(1 << 30) + 1) == L.GMLA_ERR_UNSUPPORTED
 
 
 def _norm(L, **kw):
-    a = dict(dtype=0, x=P, x_stride=64, residual=P, residual_stride=64, weight=P, eps=1e-6, T=4, d=64, residual_out=P,
+    a = dict(dtype=0, x=P, x_stride=64, residual=P, residual_stride=64, weight=P, eps=1e-6, T=4, d=64, residual_out=P + 4096,
              residual_out_stride=64, out=P, out_stride=64, codes=P, scales=P, group=32, stream=None)
     a.update(kw)
     return L.gmla_add_rms_norm(*a.values())
@@ -62,7 +64,7 @@ def _norm(L, **kw):
 
 @pytest.mark.parametrize("bad", [dict(dtype=2), dict(T=-1), dict(d=0), dict(eps=-1.0), dict(eps=float("inf")), dict(group=16),
                                  dict(group=-32), dict(group=0), dict(codes=None), dict(scales=None), dict(x=None),
-                                 dict(x=P + 2), dict(x_stride=63), dict(out_stride=0), dict(residual_stride=-64),
+                                 dict(x=P + 2), dict(residual_out=P), dict(x_stride=63), dict(out_stride=0), dict(residual_stride=-64),
                                  dict(out=None, residual_out=None, codes=None, scales=None, group=0)])
 def test_add_rms_norm(L, bad):
     assert _norm(L, **bad) == L.GMLA_ERR_INVALID_ARG
