@@ -31,7 +31,7 @@
 // decode_attn_fp8 (below), then decode_merge and the W_v GEMM of the bf16 path.
 //
 // Block scales, attention alone: 64 paged sequences, 32 heads 85 us, where reading the codes takes
-// 35; 8 sequences of 131072 rows, 128 heads 483 us, of which the MMAs of the three-term product
+// 35; 8 sequences of 131072 rows, 128 heads 485 us, of which the MMAs of the three-term product
 // and the tile's softmax take turns (the codes take 88).
 #pragma once
 #include <cuda_fp8.h>

@@ -806,8 +806,9 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1), 1) decode_attn_
 //    its epilogue). Block (0, 0) also clears that GEMM's split-K tickets.
 // ---------------------------------------------------------------------------
 // A merged latent value as `terms` bf16 terms, kDc apart. One term rounds it to 2^-8 relative; with two
-// (block scales) the W_v product reads it to 2^-16, and costs as much again as before (64
-// sequences, 32 heads: its K is 1024 instead of 512, over twice the CTAs).
+// (block scales) the W_v product, with twice the K, reads it to 2^-16; the product waits on
+// latency, so that costs nothing (64 sequences, 32 heads: 13.1 us either way), and the decode's
+// error falls from 0.0026 to 0.0020, of which the result's own rounding is 0.0017.
 __device__ __forceinline__ void store_lat(__nv_bfloat16* dst, float v, int terms) {
   const __nv_bfloat16 hi = __float2bfloat16_rn(v);
   dst[0] = hi;

@@ -27,7 +27,7 @@
 // activations are stored as fp16 too (w4_wide_prep), and the tcgen05 GEMM of the bf16 path runs on
 // them. A code times a scale has 3 + 8 significant bits, fp16's 11, so no weight is rounded (in bf16
 // each would be, by 2^-8: at 2000 tokens, 7168 x 8192, an error of 0.0027 instead of 0.0017, nearly
-// all of it the result's own rounding). What fp16 lacks is range, so each weight row and each token
+// all of it the result's own rounding). There the operands take 35 + 36 us and the GEMM 228, at 1030 TFLOP/s. What fp16 lacks is range, so each weight row and each token
 // row is first multiplied by a power of two that brings its largest element near fp16's top; the
 // GEMM's epilogue takes both back. Elements down to 2^-28 of the largest keep their full precision.
 #include <cuda_fp16.h>
@@ -509,8 +509,8 @@ static cudaError_t launch_w4_group(const W4Args& a, const W4Plan& p, cudaStream_
 
 // Token columns: the smallest of 8, 16 and 32 that holds T, or up to eight tiles of 32, which share a
 // row tile's codes in L2. More tokens are left to expansion and GEMM (us at 4096 x 4096 and 7168 x
-// 16384: 64 tokens 16.7 and 72 against 27 and 123, 128 tokens 24 and 136 against 35 and 153, 256 tokens
-// 39 and 230 against 53 and 264). K splits: the number (1 .. 8, one cluster) with the least time,
+// 16384: 64 tokens 16.7 and 73, 128 tokens 24 and 136, 256 tokens 39 and 230; expansion and GEMM take 62
+// and 267 from 257 to 512 tokens). K splits: the number (1 .. 8, one cluster) with the least time,
 // counted as waves of resident CTAs times the chunks that each works through plus about two chunks'
 // time for its start and its sum. A cluster stays within one GPC, of which some have fewer SMs, and
 // w4_prep's last CTAs still hold slots when it is placed: an eighth of the slots is left out. (One
