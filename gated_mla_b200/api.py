@@ -76,6 +76,7 @@ def _check(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device:
 
 # the current stream's handle without a Stream object around it (3 us less a call)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice     # of a process whose CUDA context exists: a CUDA tensor is at hand
 
 
 def _stream_of(t: torch.Tensor) -> int:
@@ -83,7 +84,7 @@ def _stream_of(t: torch.Tensor) -> int:
     if not t.is_cuda:
         raise ValueError("gated_mla_b200 takes CUDA tensors only")
     index = t.get_device()
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}: "
                          "call inside torch.cuda.device(...)")
     return _raw_stream(index)
@@ -198,34 +199,41 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residua
     if x.dtype not in _DT or x.dim() != 2:
         raise ValueError("x must be bfloat16 or float32 [T, d]")
     dev, (T, d) = x.device, x.shape
-    if out is None and want_out:
-        out = x.new_empty((T, d))
     if residual is None and residual_out is not None:
         raise ValueError("residual_out goes with a residual")
-    if residual is not None and residual_out is None:
-        residual_out = x.new_empty((T, d))
-    codes = scales = None
-    if fp8_group:
-        if fp8_group < 0:
-            raise ValueError("fp8_group must be 0, 32, 64, 128 or 256")
-        codes = torch.empty(T, d, dtype=torch.float8_e4m3fn, device=dev)
-        scales = torch.empty(T, -(-d // fp8_group), dtype=torch.float32, device=dev)
 
     def row(t, name):      # address and row stride
         if t is None:
             return None, 0
-        _check(t, name, x.dtype, (T, d), dev)
+        if t is not x:
+            _check(t, name, x.dtype, (T, d), dev)
         if t.is_contiguous():
             return t.data_ptr(), d
         if d > 1 and t.stride(1) != 1:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
         return t.data_ptr(), t.stride(0) if T > 1 else d
 
+    if out is None and want_out:
+        out = x.new_empty((T, d))
+        out_row = out.data_ptr(), d
+    else:
+        out_row = row(out, "out")
+    if residual is not None and residual_out is None:
+        residual_out = x.new_empty((T, d))
+        sum_row = residual_out.data_ptr(), d
+    else:
+        sum_row = row(residual_out, "residual_out")
+    codes = scales = codes_at = scales_at = None
+    if fp8_group:
+        if fp8_group < 0:
+            raise ValueError("fp8_group must be 0, 32, 64, 128 or 256")
+        codes = x.new_empty((T, d), dtype=torch.float8_e4m3fn)
+        scales = x.new_empty((T, -(-d // fp8_group)), dtype=torch.float32)
+        codes_at, scales_at = codes.data_ptr(), scales.data_ptr()
     if weight is not None:
         _check(weight, "weight", x.dtype, (d,), dev)
-    L.check(L.gmla_add_rms_norm(_DT[x.dtype], *row(x, "x"), *row(residual, "residual"), _p(weight), eps, T, d,
-                                *row(residual_out, "residual_out"), *row(out, "out"), _p(codes), _p(scales), fp8_group,
-                                stream), "gmla_add_rms_norm")
+    L.check(L.lib.gmla_add_rms_norm(_DT[x.dtype], *row(x, "x"), *row(residual, "residual"), _p(weight), eps, T, d,
+                                *sum_row, *out_row, codes_at, scales_at, fp8_group, stream), "gmla_add_rms_norm")
     return NormOut(out, residual_out, codes, scales)
 
 
