@@ -80,8 +80,10 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// CTAs that share an SM, by their shared memory and registers
-constexpr int w4_ctas_per_sm(int nt) { return nt <= 2 ? 3 : 2; }
+// CTAs that share an SM, by their shared memory and registers. (One column tile with two CTAs and a ring of
+// five stages: 23.5 us against 23.1 at 7168 x 16384. Two column tiles with three CTAs, three stages each and a
+// few spills: 29.4 us against 27.8, and 22.1 against 17.0 at 2048 x 16384.)
+constexpr int w4_ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 
 struct W4Smem {
   uint64_t full[4], empty[4];
@@ -92,7 +94,7 @@ template <int NT>   // token columns in tiles of 8: 1, 2 or 4
 struct W4Cfg {
   static constexpr int kXFrag = (kW4Chunk / 32) * NT * 512;    // [8 steps of 32 k][NT][32 lanes][16 bytes]
   static constexpr int kXBytes = kXFrag + 256 * NT;            // then -136 sums [groups of the chunk, up to 8][8 NT] fp32
-  static constexpr int kStages = 3;
+  static constexpr int kStages = NT == 2 ? 4 : 3;
   // the codes' boxes first (1024-byte aligned for the swizzle), then the activations
   static constexpr int kPitch = kW4Rows + 4;                   // floats between tokens of the partial tile
   static constexpr int kRed = kPitch * 8 * NT * 4;             // fp32 partial tile, over the ring once it has drained
@@ -509,13 +511,13 @@ static cudaError_t launch_w4_group(const W4Args& a, const W4Plan& p, cudaStream_
 
 // Token columns: the smallest of 8, 16 and 32 that holds T, or up to eight tiles of 32, which share a
 // row tile's codes in L2. More tokens are left to expansion and GEMM (us at 4096 x 4096 and 7168 x
-// 16384: 64 tokens 16.7 and 73, 128 tokens 24 and 136, 256 tokens 39 and 230; expansion and GEMM take 62
+// 16384: 64 tokens 16.7 and 73, 128 tokens 24 and 136, 256 tokens 39 and 240; expansion and GEMM take 62
 // and 267 from 257 to 512 tokens). K splits: the number (1 .. 8, one cluster) with the least time,
-// counted as waves of resident CTAs times the chunks that each works through plus about two chunks'
-// time for its start and its sum. A cluster stays within one GPC, of which some have fewer SMs, and
-// w4_prep's last CTAs still hold slots when it is placed: an eighth of the slots is left out. (One
-// token at 7168 x 16384: 392 of 444 CTAs, in clusters of 7, took 22 us in a stream but two waves and
-// 36 us in a graph; 336, in clusters of 6, take 23 and 25. 32 tokens: clusters of 5 51 us, of 4 41.)
+// counted as waves of resident clusters times the chunks that each CTA works through plus about two
+// chunks' time for its start and its sum. A cluster stays within one of the 8 GPCs, and w4_prep's last CTAs
+// still hold slots when it is placed: a sixteenth of what fits is left out. (One token at 7168 x 16384: 56
+// clusters of 7, just what fits, took 22 us in a stream but two waves and 36 us in a graph; of 6 they take 23
+// and 25. 16 tokens at 4096 x 4096: 32 of 8 13.5 us, of 6 9.6. 32 tokens at 7168 x 16384: 56 of 5 51 us, of 4 41.)
 W4Plan w4_plan(int N, int T, int K, int num_sms) {
   W4Plan p{};
   p.T8 = T;
@@ -525,10 +527,10 @@ W4Plan w4_plan(int N, int T, int K, int num_sms) {
   p.nt = T <= 8 ? 1 : (T <= 16 ? 2 : 4);
   const int token_tiles = (T + 8 * p.nt - 1) / (8 * p.nt);
   const int64_t tiles = static_cast<int64_t>((N + kW4Rows - 1) / kW4Rows) * token_tiles;
-  const int64_t slots = static_cast<int64_t>(num_sms) * w4_ctas_per_sm(p.nt) * 7 / 8;
   int64_t best = 0;
   for (int s = 1; s <= 8 && s <= chunks; ++s) {
-    const int64_t cost = ((tiles * s + slots - 1) / slots) * ((chunks + s - 1) / s + 2);
+    const int64_t fit = 8 * (num_sms / 8 * w4_ctas_per_sm(p.nt) / s), room = fit > 16 ? fit - fit / 16 : 1;
+    const int64_t cost = ((tiles + room - 1) / room) * ((chunks + s - 1) / s + 2);
     if (s == 1 || cost < best) best = cost, p.splits = s;
   }
   p.T8 = 8 * p.nt * token_tiles;
