@@ -1108,6 +1108,7 @@ gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const vo
   if (!make_tmap_2d_u8(&a.wmap, w4->codes, K / 2, N, K / 2, 128, 128))
     return fail(GMLA_ERR_CUDA, "tensor map for gate_out_w4 failed");
   a.x = act;
+  a.codes = w4->codes;
   a.scales = w4->scales;
   a.y = y;
   a.status = status;

@@ -251,6 +251,7 @@ struct W4PrepArgs {
 struct W4Args {
   CUtensorMap wmap;          // 2D [N, K / 2] bytes
   const void* x;             // w4_prep's out
+  const void* codes;         // [N, K / 2] bytes, as wmap
   const void* scales;        // [N, K / group] bf16
   void* y;                   // [T, N] bf16
   int* status;

@@ -15,7 +15,9 @@
 //     so k and k + 4 sit side by side in the activations too.
 //   * sum (v - 8) a = sum (128 + v) a - 136 sum a: the group sums of the activations
 //     come from w4_prep, in fp32, and take the place of a subtraction for every pair.
-//     (The cancellation costs 136 / 4.6, five bits of fp32's 24.)
+//     (The cancellation costs 136 / 4.6, five bits of fp32's 24. An infinity, or a value near fp32's
+//     largest, would cancel to NaN: such a group gives NaN on purpose, and each output that comes out
+//     as NaN is taken again from its definition, w4_direct.)
 //   * The products of one group are summed in fp32 and only then scaled, so no
 //     weight is ever rounded.
 // w4_prep applies the gate and stores the activations in the order in which a warp
@@ -131,6 +133,10 @@ __device__ __forceinline__ void w4_gated8(const W4PrepArgs& a, int t, int k, flo
   }
 }
 
+// Elements from here on (2^100, the bits of a bf16) make their group's sum NaN: below, 128 of them times
+// 128 + v stay within 2^115, far from fp32's largest.
+constexpr uint32_t kW4Large = 0x7180;
+
 // ---------------------------------------------------------------------------
 // a = gate ⊙ o in bf16, in fragment order, and -136 times its sum over each group.
 // out: for each token tile of 8 nt and each chunk of 256 k, [8 steps][nt][g * 4 + c][8 bf16]: token 8 n + g of the
@@ -163,6 +169,9 @@ __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) sum += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
+    const uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                  __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    if ((top & 0xffffu) >= kW4Large || (top >> 16) >= kW4Large) sum = __uint_as_float(0x7fc00000u);
     for (int o = 1; o < g8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (i < n) {
       const int tile = t / (8 * a.nt), tt = t - tile * (8 * a.nt);
@@ -173,6 +182,33 @@ __global__ void __launch_bounds__(256) w4_prep_kernel(W4PrepArgs a) {
       reinterpret_cast<uint4*>(blk)[(((k >> 5) & 7) * a.nt + (tt >> 3)) * 32 + (tt & 7) * 4 + ((k >> 3) & 3)] = r;
     }
   }
+}
+
+// ---------------------------------------------------------------------------
+// y[t, n] from its definition, in 64 bits: for outputs whose sum came out as NaN (large or infinite
+// activations; a NaN among the inputs stays one). `x`: the token tile's blocks as w4_prep lays them out,
+// tt the token in the tile. One thread an output, over all of K: slow, and rare.
+// ---------------------------------------------------------------------------
+static __device__ __noinline__ float w4_direct(const W4Args& a, const uint8_t* x, int nt, int tt, int n) {
+  const int n_groups = a.K / a.group;
+  const uint32_t* codes = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.codes) + static_cast<int64_t>(n) * (a.K >> 1));
+  const __nv_bfloat16* scales = static_cast<const __nv_bfloat16*>(a.scales) + static_cast<int64_t>(n) * n_groups;
+  double y = 0.0;
+  for (int k = 0; k < a.K && y == y; k += 8) {
+    const uint8_t* blk = x + static_cast<int64_t>(k / kW4Chunk) * (nt * W4Cfg<1>::kXBytes);
+    const uint4 r = reinterpret_cast<const uint4*>(blk)[(((k >> 5) & 7) * nt + (tt >> 3)) * 32 + (tt & 7) * 4 + ((k >> 3) & 3)];
+    const uint32_t v[4] = {r.x, r.y, r.z, r.w};      // elements q and q + 4 of the run
+    const uint32_t w = codes[k >> 3];
+    double sum = 0.0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int lo = static_cast<int>((w >> (4 * q)) & 15u) - 8, hi = static_cast<int>((w >> (4 * q + 16)) & 15u) - 8;
+      sum += static_cast<double>(__uint_as_float(v[q] << 16)) * lo;
+      sum += static_cast<double>(__uint_as_float(v[q] & 0xffff0000u)) * hi;
+    }
+    y += sum * static_cast<double>(__bfloat162float(scales[k / a.group]));
+  }
+  return static_cast<float>(y);
 }
 
 // ---------------------------------------------------------------------------
@@ -373,6 +409,14 @@ __global__ void __launch_bounds__(kW4Threads, W4Cfg<NT>::kCtas) w4_mma_kernel(co
         if (k < splits) v.x += p[k].x, v.y += p[k].y, v.z += p[k].z, v.w += p[k].w;
     } else {
       v = *reinterpret_cast<const float4*>(red + t * C::kPitch + r);
+    }
+    if (!(v.x == v.x && v.y == v.y && v.z == v.z && v.w == v.w)) {
+      const uint8_t* x = static_cast<const uint8_t*>(a.x) + static_cast<int64_t>(blockIdx.y) * n_chunk * C::kXBytes;
+      float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k)
+        if (f[k] != f[k] && row0 + r + k < a.N) f[k] = w4_direct(a, x, NT, t, row0 + r + k);
+      v = make_float4(f[0], f[1], f[2], f[3]);
     }
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + static_cast<int64_t>(t0 + t) * a.N + row0 + r;
     if (a.N % 4 == 0) {

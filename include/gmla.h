@@ -265,6 +265,8 @@ GMLA_API gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w
  * fp32: no weight is rounded. Above that weights and activations become fp16 numbers
  * under a power of two for each row, in the workspace: weights exact while the scales
  * of a row lie within 2^28 of one another, activations rounded to 2^-12.
+ * Infinities and NaN give what the formula gives, in their own row of y (0 times an infinity, a code of
+ * 8 that is, gives NaN). Activations of 2^100 and more are taken in 64 bits up to 256 tokens: slowly.
  * ------------------------------------------------------------------------- */
 GMLA_API gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4,
                                       const void* o, int32_t T, const float* gate_logits,
