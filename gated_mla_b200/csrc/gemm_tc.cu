@@ -349,11 +349,12 @@ __global__ void __launch_bounds__(192, kSwap ? 1 : 2) gemm_bf16_tc_kernel(const 
           if (a.f16) {
 #pragma unroll
             for (int j = 0; j < 16; j += 4) {
+              // the scale below 1 first: a large and a small one (2^113 and 2^-40) leave fp32's range only together
               const float4 s = *reinterpret_cast<const float4*>(a.f_scale + f0 + j);
-              x[j] = x[j] * t_scale * s.x;
-              x[j + 1] = x[j + 1] * t_scale * s.y;
-              x[j + 2] = x[j + 2] * t_scale * s.z;
-              x[j + 3] = x[j + 3] * t_scale * s.w;
+              x[j] = t_scale < 1.f ? x[j] * t_scale * s.x : x[j] * s.x * t_scale;
+              x[j + 1] = t_scale < 1.f ? x[j + 1] * t_scale * s.y : x[j + 1] * s.y * t_scale;
+              x[j + 2] = t_scale < 1.f ? x[j + 2] * t_scale * s.z : x[j + 2] * s.z * t_scale;
+              x[j + 3] = t_scale < 1.f ? x[j + 3] * t_scale * s.w : x[j + 3] * s.w * t_scale;
             }
           }
           if (e.rope) {

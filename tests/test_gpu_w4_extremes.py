@@ -10,8 +10,8 @@ from test_gpu_w4 import _make
 
 pytestmark = pytest.mark.gpu
 BIG = 3.0e38
-# a single tile of 8, 16 and 32 tokens, and several of 32
-TOKENS = [1, 5, 13, 29, 70, 256]
+# a single tile of 8, 16 and 32 tokens, several of 32, and (above 256) the product over fp16 rows
+TOKENS = [1, 5, 13, 29, 70, 256, 300]
 
 
 def _want(w4, group, o, gate=None):
