@@ -322,7 +322,8 @@ class GatedMLA:
 
     def latent_project(self, x, positions, seq_ids, cache: LatentCache, q_out=None, gate_logits=None, *,
                        cu_seqlens=None, seq_lens=None):
-        """Project the tokens and write their latents into the cache. A block-scaled cache
+        """Project the tokens and write their latents into the cache; nothing is cached for padding
+        (tokens with position and seq_id -1, as plan_batch marks them). A block-scaled cache
         takes the packing of the tokens too (``cu_seqlens`` and ``seq_lens``, as cache_append):
         the latents go through a bf16 buffer of the step's rows."""
         T = x.shape[0]

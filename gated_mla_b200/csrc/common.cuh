@@ -35,6 +35,9 @@ static __device__ __noinline__ int64_t cache_row(const CacheView& c, int b, int 
   return static_cast<int64_t>(page) * c.page_size + (pos % c.page_size);
 }
 
+// A token row behind a batch's last sequence, as gmla_plan_batch marks it: nothing is cached for it, and no fault reported.
+static __device__ __forceinline__ bool padding_row(int b, int pos) { return b == -1 && pos == -1; }
+
 // Gate modes (gmla_gate_mode): per channel, or per head as a sigmoid, hard
 // top-k, binary or ternary value.
 enum : int { kGateChannel = 0, kGateHead = 1, kGateTopk = 2, kGateBinary = 3, kGateTernary = 4 };

@@ -245,8 +245,9 @@ __global__ void __launch_bounds__(192, kSwap ? 1 : 2) gemm_bf16_tc_kernel(const 
         int pos = 0;
         if (lt < tile.ntok && (e.rope || e.cache_scatter)) pos = a.positions[tok];
         if (lt < tile.ntok && e.cache_scatter) {
-          row = cache_row(a.cache, a.seq_ids[tok], pos);
-          if (row < 0) report_status(a.status, kStatusRange);
+          const int seq = a.seq_ids[tok];
+          row = cache_row(a.cache, seq, pos);
+          if (row < 0 && !padding_row(seq, pos)) report_status(a.status, kStatusRange);
         }
         tok_row[lt] = lt < tile.ntok ? row : -1;
         tok_pos[lt] = pos;
@@ -333,8 +334,9 @@ __global__ void __launch_bounds__(192, kSwap ? 1 : 2) gemm_bf16_tc_kernel(const 
         const float t_scale = a.f16 && tok_ok ? a.t_scale[tok] : 1.f;
         if (tok_ok && (e.rope || e.cache_scatter)) pos = a.positions[tok];
         if (tok_ok && e.cache_scatter) {
-          row = cache_row(a.cache, a.seq_ids[tok], pos);
-          if (row < 0) report_status(a.status, kStatusRange);
+          const int seq = a.seq_ids[tok];
+          row = cache_row(a.cache, seq, pos);
+          if (row < 0 && !padding_row(seq, pos)) report_status(a.status, kStatusRange);
         }
 #pragma unroll 1
         for (int c0 = 0; c0 < BN; c0 += 16) {

@@ -62,9 +62,10 @@ __global__ void __launch_bounds__(512) gemm_f32_kernel(const F32Args a) {
   int64_t row = t;
   if (e.rope || e.cache_scatter) pos = a.positions[t];
   if (e.cache_scatter) {
-    row = cache_row(a.cache, a.seq_ids[t], pos);
+    const int seq = a.seq_ids[t];
+    row = cache_row(a.cache, seq, pos);
     if (row < 0) {
-      report_status(a.status, kStatusRange);
+      if (!padding_row(seq, pos)) report_status(a.status, kStatusRange);
       return;
     }
   }

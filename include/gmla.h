@@ -191,7 +191,10 @@ typedef struct gmla_w4 {
  *                ("精读笔记 03" §5.1, §5.2), two GEMMs with c^Q kept in the workspace
  *   gate_logits  [T, G] fp32: W_g x (+ b_g)
  *   workspace    device scratch of gmla_latent_project_workspace_size(cfg, T) bytes
- * Rows of the cache not addressed by (seq_id, position) are left untouched.
+ * Rows of the cache not addressed by (seq_id, position) are left untouched. A token
+ * whose seq_id and position are both -1 is padding (gmla_plan_batch): nothing is cached
+ * for it, its rows of q_out and gate_logits are computed as any other's. Any other
+ * (seq_id, position) outside the cache sets GMLA_ERR_DEVICE_RANGE and caches nothing.
  * Returns GMLA_ERR_INVALID_ARG if T < 0 or a pointer is missing/misaligned.
  * ------------------------------------------------------------------------- */
 GMLA_API gmla_status gmla_latent_project(const gmla_config* cfg, const gmla_weights* w,
@@ -290,6 +293,7 @@ GMLA_API size_t gmla_gate_out_w4_workspace_size(const gmla_config* cfg, int32_t 
  *                (neither may overlap cached_lens or new_lens: copy seq_lens for the next step)
  *   positions, seq_ids [T] int32, slots [T] int64: packed by sequence; slot = page *
  *                page_size + row. Rows behind the last sequence's get -1 in all three
+ *                (padding, which gmla_latent_project passes over)
  *   pages_used   [1] int32
  *   workspace    256 bytes (the status word)
  * A batch that cannot be (a negative length, a sequence beyond max_pages_per_seq pages,
