@@ -126,6 +126,11 @@ __global__ void __launch_bounds__(256, RPW <= 2 ? 4 : (RPW <= 4 ? 2 : 1)) cache_
       continue;
     }
     const float was = off > 0 ? a.scales[si] : 0.f;
+    if (off > 0 && !(was >= kScaleMin && was <= kScaleMax)) {   // the held codes mean nothing: no scale would mend them
+      if (lane == 0 && w == 0) report_status(a.status, kStatusRange);
+      t += run;
+      continue;
+    }
     // rows r = w + WPL * i of the block: new ones off <= r < off + run
     uint4 x[RPW][2];
     float top = 0.f;

@@ -82,8 +82,6 @@ __device__ __forceinline__ void terms_e4m3x2(float a, float b, uint32_t (&t)[n])
     }
   }
 }
-// The scales of a block-scaled cache lie in [2^-32, 2^32]; one outside (or NaN) is a fault.
-constexpr float kScaleMin = 2.3283064365386963e-10f, kScaleMax = 4294967296.f;
 // byte offset of (row, col) in a K-major tile of 128-byte rows with the 128-byte swizzle
 __device__ __forceinline__ uint32_t sw128_byte(uint32_t row, uint32_t col) {
   return row * 128u + ((((col >> 4) ^ row) & 7u) << 4) + (col & 15u);

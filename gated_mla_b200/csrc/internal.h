@@ -224,6 +224,9 @@ cudaError_t launch_add_rms_norm(NormArgs a, bool f32, int num_sms, cudaStream_t 
 int norm_vectors(int d, int T, bool f32, int num_sms);
 constexpr int kNormMaxD = 32768;   // 32 warps of 4 vectors
 
+// The scales of a block-scaled cache lie in [2^-32, 2^32]; one outside (or NaN) is a fault.
+constexpr float kScaleMin = 2.3283064365386963e-10f, kScaleMax = 4294967296.f;
+
 // ----- append to a block-scaled FP8 cache (append.cu) -----
 struct AppendArgs {
   const void* latents;       // [T, 512] bf16

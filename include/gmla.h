@@ -342,8 +342,9 @@ GMLA_API gmla_status gmla_add_rms_norm(int32_t dtype, const void* x, int64_t x_s
  * block exceeds 448 * 2^E. A block that holds rows already keeps the larger of its
  * scale and that one; when it grows, the held codes are rounded again to the new
  * scale. Rows of other blocks, and rows behind the new ones, are left as they were.
- * Sequences must not share the pages that they write. A length or page out of range
- * sets GMLA_ERR_DEVICE_RANGE and its rows are skipped; cu_seqlens[B] > T sets it too.
+ * Sequences must not share the pages that they write. A length or page out of range, and
+ * a block that holds rows under a scale outside [2^-32, 2^32] (or NaN), set
+ * GMLA_ERR_DEVICE_RANGE and those rows are skipped; cu_seqlens[B] > T sets it too.
  *   workspace    256 bytes (the status word)
  * ------------------------------------------------------------------------- */
 GMLA_API gmla_status gmla_cache_append(const gmla_config* cfg, const gmla_cache* cache,
