@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(256, RPW <= 2 ? 4 : (RPW <= 4 ? 2 : 1)) cache_
   const int cu_end = a.cu[a.B], cu_0 = a.cu[0], cu_g = a.cu[guess], cu_g1 = a.cu[guess + 1];
   if (w == 0 && t < a.T)
     prefetch_l2(static_cast<const __nv_bfloat16*>(a.latents) + static_cast<int64_t>(t) * a.stride + lane * 16);
+  if (unit == 0 && w == 0 && lane == 0 && cu_end > a.T) report_status(a.status, kStatusRange);
   const int total = min(cu_end, a.T);
   const int t_end = min(t + a.window, total);
   if (t >= t_end || t < cu_0) return;   // uniform over the unit
@@ -218,7 +219,6 @@ __global__ void __launch_bounds__(256, RPW <= 2 ? 4 : (RPW <= 4 ? 2 : 1)) cache_
     }
     t += run;
   }
-  if (unit == 0 && w == 0 && lane == 0 && a.cu[a.B] > a.T) report_status(a.status, kStatusRange);
 }
 
 cudaError_t launch_cache_append(AppendArgs a, int num_sms, cudaStream_t st) {

@@ -1,5 +1,6 @@
 """cache_append refuses what it cannot continue: the fault is reported, nothing of it is written, and the
 other sequences get their rows."""
+import numpy as np
 import pytest
 import torch
 
@@ -37,7 +38,9 @@ def test_a_block_held_under_a_bad_scale_is_left_and_reported(block, scale, paged
     model.cache_append(x, cu, torch.full((3,), held + n, dtype=torch.int32, device="cuda"), pool.cache)
     _reported(model)
     import operators_ref as R
-    R.append(pool.codes, pool.scales, pool.row_of, pool.block_of, x.double().cpu().numpy(), cu.tolist(), [held + n] * 3, block)
+    with np.errstate(all="ignore"):       # the block in question is put back below
+        R.append(pool.codes, pool.scales, pool.row_of, pool.block_of, x.double().cpu().numpy(), cu.tolist(), [held + n] * 3,
+                 block)
     # the block in question is as it was, the later blocks of the sequence are appended
     first = pool.row_of(1, block)
     pool.codes[first:first + block], pool.scales[at] = codes[first:first + block], scales[at]
@@ -56,3 +59,12 @@ def test_the_decode_after_it_still_sees_the_fault():
     other = _model(W_k=model.weights["W_k"], W_v=model.weights["W_v"])
     other.decode(torch.zeros(1, 16, 128, dtype=torch.bfloat16, device="cuda"), None, pool.cache, lens)
     _reported(other)
+
+
+def test_offsets_past_the_rows_are_reported_when_the_batch_is_a_slice_too():
+    """A slice of a packed batch: its offsets start behind 0, and end behind the rows that were given."""
+    model = _model()
+    pool = Pool(2, 64, 16, 16)
+    cu = torch.tensor([2, 4, 9], dtype=torch.int32, device="cuda")
+    model.cache_append(_latents(6, 1), cu, torch.tensor([2, 5], dtype=torch.int32, device="cuda"), pool.cache)
+    _reported(model)
