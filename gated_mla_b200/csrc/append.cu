@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(256, RPW <= 2 ? 4 : (RPW <= 4 ? 2 : 1)) cache_
   if (t >= t_end || t < cu_0) return;   // uniform over the unit
   int b = t >= cu_g && t < cu_g1 ? guess : find_seq(a.cu, a.B, t, lane);
   const CacheView& cv = a.cache;
-  const int limit = cv.paged ? cv.max_pages_per_seq * cv.page_size : cv.capacity;
+  const int limit = cache_limit(cv);
   uint8_t* codes = static_cast<uint8_t*>(cv.data);
   while (t < t_end) {
     const int c0 = a.cu[b], c1 = min(a.cu[b + 1], a.T);

@@ -21,6 +21,12 @@ struct CacheView {
   int32_t row;          // d_c + d_R
 };
 
+// Most rows a sequence may have (a wide table times a large page passes 32 bits: lengths do not).
+__host__ __device__ inline int cache_limit(const CacheView& c) {
+  const int64_t rows = c.paged ? static_cast<int64_t>(c.max_pages_per_seq) * c.page_size : c.capacity;
+  return rows < 0x7fffffff ? static_cast<int>(rows) : 0x7fffffff;
+}
+
 // Global row index of token `pos` of sequence `b`, or -1 when out of range.
 static __device__ __noinline__ int64_t cache_row(const CacheView& c, int b, int pos) {
   if (b < 0 || pos < 0) return -1;

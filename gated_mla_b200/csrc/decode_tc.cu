@@ -89,7 +89,7 @@ __device__ void decode_plan_block(const DecodeArgs& a) {
   __shared__ int s_total;
   __shared__ int s_sum, s_nz;
   const int tid = threadIdx.x;
-  const int limit = a.cache.paged ? a.cache.max_pages_per_seq * a.cache.page_size : a.cache.capacity;
+  const int limit = cache_limit(a.cache);
   if (tid == 0) s_sum = s_nz = 0;
   __syncthreads();
   for (int b = tid; b < a.B; b += blockDim.x) {

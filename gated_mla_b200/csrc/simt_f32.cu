@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_f32_kernel(const AttnF32Arg
     nkeys = a.seq_lens[b];
     t = nkeys - 1;
   }
-  const int limit = a.cv.paged ? a.cv.max_pages_per_seq * a.cv.page_size : a.cv.capacity;
+  const int limit = cache_limit(a.cv);
   __shared__ float sq[512];
   __shared__ float sqlat[kMaxDc];
   __shared__ float sp[kChunk];
