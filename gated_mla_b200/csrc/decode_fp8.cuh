@@ -22,9 +22,14 @@
 // reference m follows u_t = z_t + log2 s_t, P' = kPScaleB 2^(u - m) carries the scale
 // into the product, and the softmax sum takes 2^(u - m) / s_t. P' gets a third
 // e4m3 term, and each term is stored 32 times finer than the one before
-// (P' = hi + lo / 32 + lo2 / 1024, in columns of their own): weights 2^-23 below the
-// largest still count, as they must when one token far outweighs a long
-// context's tail. At N = 3 HG <= 96 an MMA costs what it does at 2 HG.
+// (P' = hi + lo / 32 + lo2 / 1024, in columns of their own), a grid of 2^-22 of the
+// reference. Rounding to the nearest would drop every weight below 2^-23, and with
+// them the whole tail of a long context that one token far outweighs (131071 rows at
+// 2^-23 are 1.6 % of the softmax), though the denominator counts it. So the last term is
+// rounded with an offset of each token's own, spread evenly over a step: a weight w is
+// stored as 0 or 2^-22 (the two grid points around it) in the ratio that makes a sum over
+// many tokens come out right (to a few steps in all), however small w is. At N = 3 HG <= 96 an
+// MMA costs what it does at 2 HG.
 //
 // Kernels: decode_absorb_fp8, with block scales decode_absorb_tc8 (q_lat, its scale and
 // hi/lo codes; its last block builds the split plan as decode_absorb_plan does),
@@ -50,8 +55,8 @@ constexpr int kDc8 = 512;
 constexpr float kRaise8 = 2.f;
 constexpr float kPScale = 64.f;
 // With three terms (block scales) the same P' <= 256 leaves room for a raise only every 5 log2
-// units (a raise rescales O in tensor memory, nearly a tile's time), and weights down to
-// 2^-23 of the largest count.
+// units (a raise rescales O in tensor memory, nearly a tile's time), on a grid of
+// 2^-22 of the reference.
 constexpr float kRaise8B = 5.f;
 constexpr float kPScaleB = 8.f;
 
@@ -67,18 +72,25 @@ __device__ __forceinline__ void split_e4m3(float v, uint8_t& hi, uint8_t& lo) {
   hi = to_e4m3(v);
   lo = to_e4m3(v - from_e4m3(hi));
 }
+// The rounding offset of a token's last term: up to half of E4M3's smallest step (2^-9) either way. Multiples of the
+// golden ratio, modulo 1, by position: any stretch of tokens has them nearly even.
+__device__ __forceinline__ float term_offset(int pos) {
+  return static_cast<float>(static_cast<int>(static_cast<uint32_t>(pos) * 2654435769u)) * 4.547473508864641e-13f;   // 2^-41
+}
 // Two values as e4m3 terms, `n` of them, each 32 times finer than the one before
-// (v = t0 + t1 / 32 + t2 / 1024): codes of the pair in the low two bytes of t[i].
+// (v = t0 + t1 / 32 + t2 / 1024): codes of the pair in the low two bytes of t[i]. `offset` goes to the
+// last term before it is rounded (0 stays 0).
 template <int n>
-__device__ __forceinline__ void terms_e4m3x2(float a, float b, uint32_t (&t)[n]) {
+__device__ __forceinline__ void terms_e4m3x2(float a, float b, float offset, uint32_t (&t)[n]) {
 #pragma unroll
   for (int i = 0; i < n; ++i) {
     const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
     t[i] = c;
     if (i + 1 < n) {
       const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3));
-      a = (a - __low2float(h)) * 32.f;
-      b = (b - __high2float(h)) * 32.f;
+      const float d = i + 2 == n ? offset : 0.f;
+      a = fmaf(a - __low2float(h), 32.f, d);
+      b = fmaf(b - __high2float(h), 32.f, d);
     }
   }
 }
@@ -774,8 +786,9 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
       }
       for (int t = sg.y; t < sg.z; ++t, ++ntile) {
         const bool first = (t == sg.y);
-        float lg = 0.f, isc = 1.f;
+        float lg = 0.f, isc = 1.f, offset = 0.f;
         if (BLK) {
+          offset = term_offset(t * kTok + row);
           sc = sc_next;
           sc_next = scale_of(t + 1, page_next);
           page_next = scale_page(t + 2);
@@ -901,7 +914,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
               lsum[c + j] = fmaf(p0, isc, lsum[c + j]);
               lsum[c + j + 1] = fmaf(p1, isc, lsum[c + j + 1]);
               uint32_t term[C::kTerms];
-              terms_e4m3x2<C::kTerms>(p0 * kPScaleB, p1 * kPScaleB, term);
+              terms_e4m3x2<C::kTerms>(p0 * kPScaleB, p1 * kPScaleB, offset, term);
 #pragma unroll
               for (int k = 0; k < C::kTerms; ++k) {
                 pb[sw128_byte(k * HG + h, row)] = static_cast<uint8_t>(term[k]);
