@@ -47,6 +47,7 @@ class gmla_config(ctypes.Structure):
         ("gate_topk", ctypes.c_int32),
         ("cache_dtype", ctypes.c_int32),
         ("cache_scale", ctypes.c_float),
+        ("status", ctypes.c_void_p),
     ]
 
 
@@ -112,6 +113,7 @@ def _load() -> ctypes.CDLL:
         "gmla_decode_workspace_size": (S, [cfgp, I]),
         "gmla_prefill_workspace_size": (S, [cfgp, I, I]),
         "gmla_gate_out_workspace_size": (S, [cfgp, I]),
+        "gmla_status_word": (st, [ctypes.POINTER(P)]),
         "gmla_clear_status": (st, [P, P]),
         "gmla_sync_status": (st, [P, P]),
         "gmla_status_string": (ctypes.c_char_p, [st]),
@@ -218,6 +220,13 @@ def gmla_latent_project_workspace_size(cfg, T):
 
 def gmla_gate_out_workspace_size(cfg, T):
     return lib.gmla_gate_out_workspace_size(ctypes.byref(cfg), T)
+
+
+def gmla_status_word():
+    """Address of a new status word on the current device."""
+    word = ctypes.c_void_p()
+    check(lib.gmla_status_word(ctypes.byref(word)), "gmla_status_word")
+    return word.value
 
 
 def gmla_clear_status(ws, stream):

@@ -90,41 +90,69 @@ def _stream_of(t: torch.Tensor) -> int:
     return _raw_stream(index)
 
 
+class _Memory:
+    """256 bytes of the library's device memory, for torch."""
+
+    def __init__(self, address: int):
+        self.__cuda_array_interface__ = dict(shape=(256,), typestr="|u1", data=(address, False), version=3)
+
+
 class _Scratch:
-    """Workspaces by (call, stream): calls on different streams never share one, and a
-    call under graph capture gets one of its own, which belongs to that graph."""
+    """Device memory of the calls. Workspaces go by (call, device, stream): calls on different
+    streams never share one, and a call under graph capture gets one of its own, which belongs to
+    that graph. Status words go by (call, device) and stay: captured calls record their faults in
+    them too, where sync_status finds them."""
 
     def __init__(self):
         self._held = {}
 
     def get(self, key: str, nbytes: int, device: torch.device, stream: int) -> torch.Tensor:
-        """At least `nbytes` bytes whose status word was zeroed when they were made."""
-        capturing = torch.cuda.is_current_stream_capturing()
-        held = None if capturing else self._held.get((key, device.index, stream))
-        if held is not None and held.numel() >= nbytes:
-            return held
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        if held is None:
-            L.check(L.gmla_clear_status(ws.data_ptr(), stream), "clear_status")
-        else:
-            ws[:4].copy_(held[:4])       # what it has recorded stays to be reported
-        if not capturing:
-            self._held[(key, device.index, stream)] = ws
+        """At least `nbytes` bytes, of any content."""
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = self._held.get((key, device.index, stream))
+        if ws is None or ws.numel() < nbytes:
+            ws = self._held[(key, device.index, stream)] = torch.empty(nbytes, dtype=torch.uint8, device=device)
         return ws
 
+    def word(self, key: str, device: torch.device) -> torch.Tensor:
+        """256 bytes that begin with a status word, zero at first."""
+        word = self._held.get((key, device.index))
+        if word is None:
+            with torch.cuda.device(device):
+                word = torch.as_tensor(_Memory(L.gmla_status_word()), device=device)
+            self._held[(key, device.index)] = word
+        return word
+
+    def words(self):
+        return [(key[0], ws) for key, ws in list(self._held.items()) if len(key) == 2]
+
     def sync_status(self) -> None:
-        for (key, index, stream), ws in self._held.items():
-            with torch.cuda.device(index):
-                L.check(L.gmla_sync_status(ws.data_ptr(), stream), f"device status ({key})")
+        for key, word in self.words():
+            with torch.cuda.device(word.device):
+                torch.cuda.synchronize()
+                L.check(L.gmla_sync_status(word.data_ptr(), None), f"device status ({key})")
+
+    def clear_status(self) -> None:
+        for _, word in self.words():
+            with torch.cuda.device(word.device):
+                torch.cuda.synchronize()       # what was launched before is not to report afterwards
+                L.check(L.gmla_clear_status(word.data_ptr(), None), "clear_status")
+                torch.cuda.synchronize()
 
 
 _scratch = _Scratch()
 
 
 def sync_status() -> None:
-    """Synchronise and raise if a plan_batch call reported a batch that cannot be. Calls captured
-    into a graph have workspaces of their own, which this does not read."""
+    """Synchronise and raise if a plan_batch call, captured ones included, reported a batch that cannot
+    be. The report stays until clear_status."""
     _scratch.sync_status()
+
+
+def clear_status() -> None:
+    """Synchronise and forget what plan_batch calls have reported."""
+    _scratch.clear_status()
 
 
 class BatchPlan:
@@ -153,7 +181,7 @@ def plan_batch(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     new_lens; rows behind the last sequence get -1. ``out`` reuses the buffers of an
     earlier plan of the same sizes (copy its ``seq_lens`` first when they are this
     step's ``cached_lens``). A batch that does not fit is planned as empty and
-    reported by ``sync_status``.
+    reported by ``sync_status`` until ``clear_status``.
     """
     dev, B, T = cached_lens.device, cached_lens.shape[0], n_tokens
     stream = _stream_of(cached_lens)
@@ -169,7 +197,7 @@ def plan_batch(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
         out = BatchPlan(B, T, dev)
     elif out._sizes != (B, T, dev):
         raise ValueError(f"out is a plan of {out._sizes}, this batch is {(B, T, dev)}")
-    ws = _scratch.get("plan_batch", 256, dev, stream)
+    ws = _scratch.word("plan_batch", dev)
     L.check(L.lib.gmla_plan_batch(
         _p(cached_lens), _p(new_lens), B, _p(free_pages), n_free, page_size, _p(block_table), M, T,
         out.seq_lens.data_ptr(), out.cu_seqlens.data_ptr(), out.positions.data_ptr(), out.seq_ids.data_ptr(),
@@ -292,7 +320,7 @@ class GatedMLA:
             setattr(self.w, k, _p(self.weights.get(k)))
         self._ws = {}
         self._scratch = _Scratch()
-        self._staging_cfg = None
+        self._cfgs = {}
 
     # -- sizes
     @property
@@ -310,6 +338,17 @@ class GatedMLA:
             self._ws[key] = ws
             L.check(L.gmla_clear_status(ws.data_ptr(), torch.cuda.current_stream().cuda_stream), "clear_status")
         return ws
+
+    def _status_cfg(self, device: torch.device, staging: bool = False) -> L.gmla_config:
+        """The configuration with the layer's status word on the device; `staging`: the same layer over a bf16 cache."""
+        cfg = self._cfgs.get((device.index, staging))
+        if cfg is None:
+            cfg = L.gmla_config.from_buffer_copy(self.cfg)
+            cfg.status = self._scratch.word("layer", device).data_ptr()
+            if staging:
+                cfg.cache_dtype = L.GMLA_CACHE_SAME
+            self._cfgs[(device.index, staging)] = cfg
+        return cfg
 
     @staticmethod
     def _stream() -> int:
@@ -348,7 +387,9 @@ class GatedMLA:
             o_out = torch.empty(B, c.n_heads * c.d_h, dtype=self.dtype, device=q.device)
         nb = L.gmla_decode_workspace_size(c, B)
         if ws is None and self.block_scaled:
-            ws = self._scratch.get("decode", nb, q.device, _stream_of(q))
+            stream = _stream_of(q)
+            c = self._status_cfg(q.device)
+            ws = self._scratch.get("decode", nb, q.device, stream)
         if ws is None:
             ws = self.workspace("decode", nb, q.device)
         L.check(L.gmla_decode(c, self.w, _p(q), _p(gate_logits), cache.struct(), _p(seq_lens), B,
@@ -394,7 +435,7 @@ class GatedMLA:
         _check(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
         if latents.stride(1) != 1:
             raise ValueError("latents: the elements of a row must be contiguous")
-        ws = self._scratch.get("append", 256, dev, stream)
+        ws = self._scratch.word("layer", dev)
         L.check(L.gmla_cache_append(c, self._cache_struct(cache, dev), latents.data_ptr(),
                                     latents.stride(0) if T > 1 else c.d_c, _p(cu_seqlens), _p(seq_lens), B, T,
                                     ws.data_ptr(), ws.numel(), stream), "gmla_cache_append")
@@ -412,11 +453,7 @@ class GatedMLA:
             raise ValueError("a block-scaled cache needs cu_seqlens and seq_lens")
         stream = _stream_of(x)
         T, dev = x.shape[0], x.device
-        if self._staging_cfg is None:      # the same layer over a bf16 cache: one sequence, row t the latent of token t
-            cfg = L.gmla_config.from_buffer_copy(self.cfg)
-            cfg.cache_dtype = L.GMLA_CACHE_SAME
-            self._staging_cfg = cfg
-        cfg = self._staging_cfg
+        cfg = self._status_cfg(dev, staging=True)      # over a bf16 cache of one sequence, row t the latent of token t
         if cfg.d_rope:
             raise ValueError("a block-scaled cache covers NoPE")
         if q_out is None:
@@ -436,7 +473,8 @@ class GatedMLA:
     def gate_out_w4(self, o, w4: W4Weight, gate_logits=None, y_out=None):
         """gate_out with W_o in 4 bits (``w4`` is [d_model, H*d_h])."""
         stream = _stream_of(o)
-        c, dev, T = self.cfg, o.device, o.shape[0]
+        dev, T = o.device, o.shape[0]
+        c = self._status_cfg(dev)
         K = c.n_heads * c.d_h
         _check(o, "o", self.dtype, (T, K), dev)
         if w4.group not in (32, 64, 128) or K % w4.group:
@@ -455,10 +493,17 @@ class GatedMLA:
         return y_out
 
     def sync_status(self):
-        """Synchronise and raise if any kernel reported a device-side fault."""
+        """Synchronise and raise if any kernel of the layer's calls, captured ones included, reported a
+        device-side fault. The report stays until clear_status."""
         self._scratch.sync_status()
         for key, ws in self._ws.items():
             L.check(L.gmla_sync_status(ws.data_ptr(), self._stream()), f"device status ({key})")
+
+    def clear_status(self):
+        """Synchronise and forget what the layer's calls have reported."""
+        self._scratch.clear_status()
+        for ws in self._ws.values():
+            L.check(L.gmla_clear_status(ws.data_ptr(), self._stream()), "clear_status")
 
     # -- whole steps
     def decode_step(self, x, cache: LatentCache, seq_lens, positions, seq_ids, *, cu_seqlens=None,

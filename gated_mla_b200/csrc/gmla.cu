@@ -103,6 +103,7 @@ gmla_status check_cfg(const gmla_config* c) {
   if (!(c->softmax_scale > 0.f) || !std::isfinite(c->softmax_scale))
     return fail(GMLA_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
   if (c->d_rope && !(c->rope_base > 1.f)) return fail(GMLA_ERR_INVALID_ARG, "rope_base must be > 1");
+  if (reinterpret_cast<uintptr_t>(c->status) % 4) return fail(GMLA_ERR_INVALID_ARG, "status is not 4-byte aligned");
   return GMLA_OK;
 }
 
@@ -123,6 +124,7 @@ bool cfg_valid(const gmla_config* c) {
   if (c->dtype != GMLA_BF16 && c->dtype != GMLA_FP32) return false;
   if (!(c->softmax_scale > 0.f) || !std::isfinite(c->softmax_scale)) return false;
   if (c->d_rope && !(c->rope_base > 1.f)) return false;
+  if (reinterpret_cast<uintptr_t>(c->status) % 4) return false;
   return true;
 }
 
@@ -188,6 +190,9 @@ CacheView cache_view(const gmla_config* c, const gmla_cache* k) {
 
 // bf16 terms of a merged latent value: see store_lat (decode_tc.cu)
 int lat_terms(const gmla_config* c) { return c->cache_dtype == GMLA_CACHE_FP8_BLOCK ? 2 : 1; }
+
+// Where a call's kernels record a fault.
+int* status_of(const gmla_config* c, void* workspace) { return c->status ? c->status : static_cast<int*>(workspace); }
 
 int gate_width(const gmla_config* c) {
   return c->gate_mode == GMLA_GATE_CHANNEL ? c->n_heads * c->d_h : c->n_heads;
@@ -409,6 +414,42 @@ gmla_status gmla_sync_status(const void* workspace, void* stream) {
   return v == 0 ? GMLA_OK : fail(GMLA_ERR_CUDA, "unknown device status %d", v);
 }
 
+// Status words outside any workspace: slabs of device memory, 256 bytes a word.
+gmla_status gmla_status_word(int32_t** word) {
+  constexpr int kWordBytes = 256, kSlabWords = 256, kDevices = 64;
+  struct Slab {
+    uint8_t* base;
+    int used;
+  };
+  static std::mutex mu;
+  static Slab slabs[kDevices] = {};
+  if (!word) return fail(GMLA_ERR_INVALID_ARG, "word is NULL");
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "gmla_status_word");
+  if (dev < 0 || dev >= kDevices) return fail(GMLA_ERR_UNSUPPORTED, "device ordinal out of range");
+  std::lock_guard<std::mutex> lk(mu);
+  Slab& s = slabs[dev];
+  if (!s.base || s.used == kSlabWords) {
+    // a stream of this thread may be under capture: the allocation and the zeros are no part of its graph
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    void* p = nullptr;
+    cudaStream_t st = nullptr;
+    e = cudaMalloc(&p, static_cast<size_t>(kSlabWords) * kWordBytes);
+    if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
+    if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, static_cast<size_t>(kSlabWords) * kWordBytes, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (st) cudaStreamDestroy(st);
+    if (e != cudaSuccess && p) cudaFree(p);
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return cuda_fail(e, "gmla_status_word");
+    s = Slab{static_cast<uint8_t*>(p), 0};
+  }
+  *word = reinterpret_cast<int32_t*>(s.base + static_cast<size_t>(s.used++) * kWordBytes);
+  return GMLA_OK;
+}
+
 // ---------------------------------------------------------------------------
 }  // extern "C"
 
@@ -527,7 +568,7 @@ gmla_status gmla_latent_project(const gmla_config* cfg, const gmla_weights* w, c
   const int row = dc + dr, G = gate_width(cfg);
   const int dq = dh + dr;
   const CacheView cv = cache_view(cfg, cache);
-  int* status = static_cast<int*>(workspace);
+  int* status = status_of(cfg, workspace);
   const bool f32 = cfg->dtype == GMLA_FP32;
   void* cq = static_cast<uint8_t*>(workspace) + 256;   // c^Q [T, d_cq] when the query is compressed
 
@@ -593,7 +634,7 @@ static gmla_status decode_impl(const gmla_config* cfg, const gmla_weights* w, co
   if (!partial_out) GMLA_TRY(check_ptr(w->W_v, "W_v"));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const CacheView cv = cache_view(cfg, cache);
-  int* status = static_cast<int*>(workspace);
+  int* status = status_of(cfg, workspace);
 
   if (cfg->dtype == GMLA_FP32 && (partial_out || seq_starts))
     return fail(GMLA_ERR_UNSUPPORTED, "context-parallel decode covers the bf16 path");
@@ -833,7 +874,7 @@ gmla_status gmla_decode_merge(const gmla_config* cfg, const gmla_weights* w, con
   g.act_group_stride = B;
   g.splits = sp.splits;
   g.kb_per_split = sp.kb_per_split;
-  g.status = static_cast<int*>(workspace);
+  g.status = status_of(cfg, workspace);
   e = launch_gemm_bf16(g, true, sp.bn, sp.ttiles, st, "gemm_wv_gate");
   return e == cudaSuccess ? GMLA_OK : cuda_fail(e, "decode_merge: W_v");
 }
@@ -864,7 +905,7 @@ gmla_status gmla_prefill(const gmla_config* cfg, const gmla_weights* w, const vo
   GMLA_TRY(check_ptr(w->W_k, "W_k"));
   GMLA_TRY(check_ptr(w->W_v, "W_v"));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int* status = static_cast<int*>(workspace);
+  int* status = status_of(cfg, workspace);
   const CacheView cv = cache_view(cfg, cache);
 
   if (cfg->dtype == GMLA_FP32) {
@@ -1016,7 +1057,7 @@ gmla_status gmla_gate_out(const gmla_config* cfg, const gmla_weights* w, const v
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int HD = cfg->n_heads * cfg->d_h, dm = cfg->d_model;
   const bool f32 = cfg->dtype == GMLA_FP32;
-  int* status = static_cast<int*>(workspace);
+  int* status = status_of(cfg, workspace);
   const void* src = o;
   if (gate_logits) {
     void* tmp = static_cast<uint8_t*>(workspace) + 256;
@@ -1085,7 +1126,7 @@ gmla_status gmla_gate_out_w4(const gmla_config* cfg, const gmla_w4* w4, const vo
   GMLA_TRY(check_ptr(gate_logits, "gate_logits", false));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int N = cfg->d_model, K = static_cast<int>(HD64), sms = num_sms();
-  int* status = static_cast<int*>(workspace);
+  int* status = status_of(cfg, workspace);
   uint8_t* act = static_cast<uint8_t*>(workspace) + 256;
   const W4Plan plan = w4_plan(N, T, K, sms);
   W4PrepArgs p{o,        gate_logits,    act,            T,         K,       cfg->n_heads,
@@ -1252,7 +1293,7 @@ gmla_status gmla_cache_append(const gmla_config* cfg, const gmla_cache* cache, c
   a.seq_lens = seq_lens;
   a.scales = cache->scales;
   a.cache = cache_view(cfg, cache);
-  a.status = static_cast<int*>(workspace);
+  a.status = status_of(cfg, workspace);
   a.B = B;
   a.T = T;
   a.scale_block = cache->scale_block;

@@ -30,7 +30,8 @@
  *     default stream). The returned status covers argument checks and the
  *     launches. Faults seen by a kernel (a device wait that timed out, a
  *     sequence longer than its cache) are written to a status word at the start
- *     of `workspace` and returned by gmla_sync_status().
+ *     of `workspace`, or to the config's `status` where that is given, and returned
+ *     by gmla_sync_status().
  *   - Row-major layouts. Weights are [out, in]:
  *       W_c [d_c, d_model]   W_kr [d_R, d_model]    W_q [H*d_h, d_model]
  *       W_qr [H*d_R, d_model]  W_k, W_v [H, d_h, d_c]
@@ -129,6 +130,8 @@ typedef struct gmla_config {
   int32_t gate_topk;      /* k of GMLA_GATE_HEAD_TOPK (1 <= k <= H); ignored otherwise */
   int32_t cache_dtype;    /* gmla_cache_dtype: the latent cache's element format */
   float cache_scale;      /* GMLA_CACHE_FP8_E4M3: a stored code e means cache_scale * e */
+  int32_t* status;        /* device word that takes the calls' faults in the workspace's place (a workspace
+                             then holds nothing from one call to the next), or NULL */
 } gmla_config;
 
 typedef struct gmla_weights {
@@ -426,6 +429,12 @@ GMLA_API size_t gmla_latent_project_workspace_size(const gmla_config* cfg, int32
 GMLA_API size_t gmla_decode_workspace_size(const gmla_config* cfg, int32_t B);
 GMLA_API size_t gmla_prefill_workspace_size(const gmla_config* cfg, int32_t T, int32_t B);
 GMLA_API size_t gmla_gate_out_workspace_size(const gmla_config* cfg, int32_t T);
+
+/* A status word outside any workspace: 256 bytes of the current device's memory whose first
+ * word is zero, for gmla_config.status or as the workspace of a call that needs only those
+ * (*word is a host pointer to the device address). Kept until the process exits. May be called
+ * while a stream is under capture: the memory is no part of the graph. */
+GMLA_API gmla_status gmla_status_word(int32_t** word);
 
 /* Zero the status word of a workspace (stream-ordered). */
 GMLA_API gmla_status gmla_clear_status(void* workspace, void* stream);
