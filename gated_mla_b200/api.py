@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import dataclasses
 import math
+import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -101,10 +102,14 @@ class _Scratch:
     """Device memory of the calls. Workspaces go by (call, device, stream): calls on different
     streams never share one, and a call under graph capture gets one of its own, which belongs to
     that graph. Status words go by (call, device) and stay: captured calls record their faults in
-    them too, where sync_status finds them."""
+    them too, where sync_status finds them.
+
+    `lock` is held from get() to the end of the call that uses the workspace: threads that share a
+    stream then share its workspaces too, one call's kernels enqueued whole before the next's."""
 
     def __init__(self):
         self._held = {}
+        self.lock = threading.Lock()
 
     def get(self, key: str, nbytes: int, device: torch.device, stream: int) -> torch.Tensor:
         """At least `nbytes` bytes, of any content."""
@@ -119,9 +124,10 @@ class _Scratch:
         """256 bytes that begin with a status word, zero at first."""
         word = self._held.get((key, device.index))
         if word is None:
-            with torch.cuda.device(device):
-                word = torch.as_tensor(_Memory(L.gmla_status_word()), device=device)
-            self._held[(key, device.index)] = word
+            with self.lock, torch.cuda.device(device):
+                word = self._held.get((key, device.index))      # another thread's, by now
+                if word is None:
+                    word = self._held[(key, device.index)] = torch.as_tensor(_Memory(L.gmla_status_word()), device=device)
         return word
 
     def words(self):
@@ -389,7 +395,11 @@ class GatedMLA:
         if ws is None and self.block_scaled:
             stream = _stream_of(q)
             c = self._status_cfg(q.device)
-            ws = self._scratch.get("decode", nb, q.device, stream)
+            with self._scratch.lock:
+                ws = self._scratch.get("decode", nb, q.device, stream)
+                L.check(L.gmla_decode(c, self.w, _p(q), _p(gate_logits), cache.struct(), _p(seq_lens), B,
+                                      _p(o_out), ws.data_ptr(), ws.numel(), stream), "gmla_decode")
+            return o_out
         if ws is None:
             ws = self.workspace("decode", nb, q.device)
         L.check(L.gmla_decode(c, self.w, _p(q), _p(gate_logits), cache.struct(), _p(seq_lens), B,
@@ -464,9 +474,10 @@ class GatedMLA:
         staging = LatentCache(rows.view(1, max(T, 1), cfg.d_c))
         order = torch.arange(T, dtype=torch.int32, device=dev)
         slot = torch.zeros(T, dtype=torch.int32, device=dev)
-        ws = self._scratch.get("project", L.gmla_latent_project_workspace_size(cfg, T), dev, stream)
-        L.check(L.gmla_latent_project(cfg, self.w, _p(x), T, _p(order), _p(slot), staging.struct(), _p(q_out),
-                                      _p(gate_logits), ws.data_ptr(), ws.numel(), stream), "gmla_latent_project")
+        with self._scratch.lock:
+            ws = self._scratch.get("project", L.gmla_latent_project_workspace_size(cfg, T), dev, stream)
+            L.check(L.gmla_latent_project(cfg, self.w, _p(x), T, _p(order), _p(slot), staging.struct(), _p(q_out),
+                                          _p(gate_logits), ws.data_ptr(), ws.numel(), stream), "gmla_latent_project")
         self.cache_append(rows[:T], cu_seqlens, seq_lens, cache)
         return q_out, gate_logits
 
@@ -487,9 +498,10 @@ class GatedMLA:
             y_out = torch.empty(T, c.d_model, dtype=self.dtype, device=dev)
         else:
             _check(y_out, "y_out", self.dtype, (T, c.d_model), dev)
-        ws = self._scratch.get("gate_out_w4", L.gmla_gate_out_w4_workspace_size(c, T), dev, stream)
-        L.check(L.gmla_gate_out_w4(c, w4.struct(), _p(o), T, _p(gate_logits), _p(y_out), ws.data_ptr(), ws.numel(),
-                                   stream), "gmla_gate_out_w4")
+        with self._scratch.lock:
+            ws = self._scratch.get("gate_out_w4", L.gmla_gate_out_w4_workspace_size(c, T), dev, stream)
+            L.check(L.gmla_gate_out_w4(c, w4.struct(), _p(o), T, _p(gate_logits), _p(y_out), ws.data_ptr(), ws.numel(),
+                                       stream), "gmla_gate_out_w4")
         return y_out
 
     def sync_status(self):
