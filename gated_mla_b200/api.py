@@ -11,6 +11,7 @@ from __future__ import annotations
 import dataclasses
 import math
 import threading
+import weakref
 from typing import NamedTuple, Optional
 
 import torch
@@ -148,6 +149,18 @@ class _Scratch:
 
 
 _scratch = _Scratch()
+_layers_scratch = lambda: None       # noqa: E731  (a weak reference once there is a layer)
+
+
+def _shared_scratch() -> _Scratch:
+    """The workspaces that all layers share, as long as there are any: the largest workspace of a call
+    holds a whole weight (gate_out_w4 above 256 tokens), which a model has room for once, not in each layer."""
+    global _layers_scratch
+    shared = _layers_scratch()
+    if shared is None:
+        shared = _Scratch()
+        _layers_scratch = weakref.ref(shared)
+    return shared
 
 
 def sync_status() -> None:
@@ -325,7 +338,8 @@ class GatedMLA:
         for k in ("W_c", "W_kr", "W_q", "W_qr", "W_k", "W_v", "W_g", "b_g", "W_o", "W_dq", "W_uq"):
             setattr(self.w, k, _p(self.weights.get(k)))
         self._ws = {}
-        self._scratch = _Scratch()
+        self._scratch = _shared_scratch()     # workspaces of the calls that report into the layer's word
+        self._status = _Scratch()             # that word
         self._cfgs = {}
 
     # -- sizes
@@ -350,7 +364,7 @@ class GatedMLA:
         cfg = self._cfgs.get((device.index, staging))
         if cfg is None:
             cfg = L.gmla_config.from_buffer_copy(self.cfg)
-            cfg.status = self._scratch.word("layer", device).data_ptr()
+            cfg.status = self._status.word("layer", device).data_ptr()
             if staging:
                 cfg.cache_dtype = L.GMLA_CACHE_SAME
             self._cfgs[(device.index, staging)] = cfg
@@ -445,7 +459,7 @@ class GatedMLA:
         _check(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
         if latents.stride(1) != 1:
             raise ValueError("latents: the elements of a row must be contiguous")
-        ws = self._scratch.word("layer", dev)
+        ws = self._status.word("layer", dev)
         L.check(L.gmla_cache_append(c, self._cache_struct(cache, dev), latents.data_ptr(),
                                     latents.stride(0) if T > 1 else c.d_c, _p(cu_seqlens), _p(seq_lens), B, T,
                                     ws.data_ptr(), ws.numel(), stream), "gmla_cache_append")
@@ -507,13 +521,13 @@ class GatedMLA:
     def sync_status(self):
         """Synchronise and raise if any kernel of the layer's calls, captured ones included, reported a
         device-side fault. The report stays until clear_status."""
-        self._scratch.sync_status()
+        self._status.sync_status()
         for key, ws in self._ws.items():
             L.check(L.gmla_sync_status(ws.data_ptr(), self._stream()), f"device status ({key})")
 
     def clear_status(self):
         """Synchronise and forget what the layer's calls have reported."""
-        self._scratch.clear_status()
+        self._status.clear_status()
         for ws in self._ws.values():
             L.check(L.gmla_clear_status(ws.data_ptr(), self._stream()), "clear_status")
 

@@ -74,3 +74,26 @@ def test_two_threads_of_a_layer_take_turns(calls, what):
     layer = _layer()
     _run([_work(layer, what)] * 2)
     assert calls["done"] == 10 and calls["clashes"] == 0
+
+
+@pytest.mark.parametrize("what", ["gate_out_w4", "decode", "latent_project"])
+def test_two_layers_in_two_threads_take_turns(calls, what):
+    """Layers share workspaces."""
+    _run([_work(_layer(), what), _work(_layer(), what)])
+    assert calls["done"] == 10 and calls["clashes"] == 0
+
+
+def test_layers_share_their_workspaces_while_there_are_layers(monkeypatch):
+    import gc
+
+    from gated_mla_b200 import api
+    monkeypatch.setattr(api, "_layers_scratch", lambda: None)
+    a, b = _layer(), _layer()
+    assert a._scratch is b._scratch and a._status is not b._status
+    ref = api._layers_scratch
+    del a
+    gc.collect()
+    assert ref() is b._scratch
+    del b
+    gc.collect()
+    assert ref() is None
