@@ -134,8 +134,8 @@ gmla_status check_ptr(const void* p, const char* name, bool required = true) {
   return GMLA_OK;
 }
 
-// Request lengths and lists of pages are read word by word, so a batch or a pool may be a slice.
-gmla_status check_words(const void* p, const char* name, bool required) {
+// Request lengths, lists of pages and block tables are read word by word, so a batch or a pool may be a slice.
+gmla_status check_words(const void* p, const char* name, bool required = true) {
   if (!p) return required ? fail(GMLA_ERR_INVALID_ARG, "%s is NULL", name) : GMLA_OK;
   if (reinterpret_cast<uintptr_t>(p) % 4) return fail(GMLA_ERR_INVALID_ARG, "%s is not 4-byte aligned", name);
   return GMLA_OK;
@@ -154,7 +154,7 @@ gmla_status check_cache(const gmla_config* c, const gmla_cache* k) {
   if (!k->paged) {
     if (k->capacity <= 0) return fail(GMLA_ERR_INVALID_ARG, "cache.capacity must be > 0");
   } else {
-    GMLA_TRY(check_ptr(k->block_table, "cache.block_table"));
+    GMLA_TRY(check_words(k->block_table, "cache.block_table"));
     if (k->page_size <= 0 || k->num_pages <= 0 || k->max_pages_per_seq <= 0)
       return fail(GMLA_ERR_INVALID_ARG, "paged cache sizes must be > 0");
     const int ps = k->page_size;
@@ -1184,7 +1184,7 @@ gmla_status gmla_plan_batch(const int32_t* cached_lens, const int32_t* new_lens,
   GMLA_TRY(check_words(cached_lens, "cached_lens", B > 0));
   GMLA_TRY(check_words(new_lens, "new_lens", B > 0));
   GMLA_TRY(check_words(free_pages, "free_pages", n_free > 0));
-  GMLA_TRY(check_ptr(block_table, "block_table", B > 0));
+  GMLA_TRY(check_words(block_table, "block_table", B > 0));
   GMLA_TRY(check_ptr(seq_lens, "seq_lens", B > 0));
   GMLA_TRY(check_ptr(cu_seqlens, "cu_seqlens"));
   GMLA_TRY(check_ptr(positions, "positions", T > 0));

@@ -44,7 +44,8 @@
  *   - The bf16 path runs on tcgen05 tensor cores with fp32 accumulation; the
  *     fp32 path runs on CUDA cores in fp32. There is no CPU fallback: a shape
  *     the kernels do not cover returns GMLA_ERR_UNSUPPORTED.
- *   - All base pointers must be 16-byte aligned.
+ *   - All base pointers must be 16-byte aligned. Block tables, and what gmla_plan_batch says
+ *     of its own arguments, may start at any element: a batch may be a slice of a larger one.
  */
 #ifndef GMLA_H_
 #define GMLA_H_
@@ -288,9 +289,9 @@ GMLA_API size_t gmla_gate_out_w4_workspace_size(const gmla_config* cfg, int32_t 
  *   new_lens     [B] int32: tokens each sequence gets in this step (0 is allowed)
  *   free_pages   [n_free] int32: unused page ids; the first *pages_used are taken,
  *                in the order of the sequences
- *   (these three may start at any element, so a batch or a pool may be a slice)
  *   block_table  [B, max_pages_per_seq] int32, in and out: entries of the pages that
  *                a sequence's new rows begin are written, all others are left as they were
+ *   (these four may start at any element, so a batch or a pool may be a slice)
  *   T            token rows of the outputs (>= the sum of new_lens)
  *   seq_lens     [B] = cached + new;  cu_seqlens [B+1] = prefix sums of new_lens
  *                (neither may overlap cached_lens or new_lens: copy seq_lens for the next step)
