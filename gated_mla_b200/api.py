@@ -239,8 +239,8 @@ def add_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residua
 
     Rows may be strided (their elements contiguous). With ``fp8_group`` (32, 64, 128 or
     256) y also comes as E4M3 codes with one scale for each group of columns;
-    ``want_out=False`` then leaves the unquantised y out. ``residual_out`` may be
-    ``residual`` itself, ``out`` may be ``x``.
+    ``want_out=False`` then leaves the unquantised y out. ``residual_out`` and ``out`` may be
+    ``residual`` or ``x`` itself (one each); any other overlap is refused.
     """
     stream = _stream_of(x)
     if x.dtype not in _DT or x.dim() != 2:

@@ -1218,6 +1218,24 @@ gmla_status gmla_plan_batch(const int32_t* cached_lens, const int32_t* new_lens,
 }
 
 // ---------------------------------------------------------------------------
+// T rows of `len` bytes, `step` bytes apart (0: a single row).
+struct RowSpan {
+  const void* p;
+  int64_t len, step;
+  const char* name;
+};
+
+// Whether no byte is in both: apart, or side by side in one matrix (the same step).
+static bool rows_disjoint(const RowSpan& a, const RowSpan& b, int64_t T) {
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t ea = pa + (T - 1) * a.step + a.len, eb = pb + (T - 1) * b.step + b.len;
+  if (ea <= pb || eb <= pa) return true;
+  if (T < 2 || (a.step && a.step != b.step)) return false;
+  const uintptr_t step = static_cast<uintptr_t>(b.step);
+  const int64_t gap = static_cast<int64_t>(pb >= pa ? (pb - pa) % step : (step - (pa - pb) % step) % step);
+  return gap >= a.len && gap + b.len <= b.step;
+}
+
 gmla_status gmla_add_rms_norm(int32_t dtype, const void* x, int64_t x_stride, const void* residual,
                               int64_t residual_stride, const void* weight, float eps, int32_t T, int32_t d,
                               void* residual_out, int64_t residual_out_stride, void* out, int64_t out_stride,
@@ -1232,7 +1250,6 @@ gmla_status gmla_add_rms_norm(int32_t dtype, const void* x, int64_t x_stride, co
   if ((group != 0) != (codes != nullptr) || (group != 0) != (scales != nullptr))
     return fail(GMLA_ERR_INVALID_ARG, "codes and scales go with a group > 0");
   if (!out && !residual_out && !codes) return fail(GMLA_ERR_INVALID_ARG, "no output is given");
-  if (out && out == residual_out) return fail(GMLA_ERR_INVALID_ARG, "out and residual_out are the same rows");
   GMLA_TRY(check_ptr(x, "x"));
   GMLA_TRY(check_ptr(residual, "residual", false));
   GMLA_TRY(check_ptr(weight, "weight", false));
@@ -1247,6 +1264,27 @@ gmla_status gmla_add_rms_norm(int32_t dtype, const void* x, int64_t x_stride, co
     if (!r.p) continue;
     if (r.s < d && T > 1) return fail(GMLA_ERR_INVALID_ARG, "a row stride is smaller than d");
     vec = vec && (T == 1 || r.s % (dtype == GMLA_FP32 ? 4 : 8) == 0);
+  }
+  // A thread reads its elements of x and residual before it stores them, so rows may be written in place; rows that
+  // overlap in any other way would be read by one thread after another has written them.
+  const int64_t es = dtype == GMLA_FP32 ? 4 : 2, n_group = group ? (d + group - 1) / group : 0;
+  const RowSpan in[3] = {{x, d * es, x_stride * es, "x"},
+                         {residual, d * es, residual_stride * es, "residual"},
+                         {weight, d * es, 0, "weight"}};
+  const RowSpan outs[4] = {{residual_out, d * es, residual_out_stride * es, "residual_out"},
+                           {out, d * es, out_stride * es, "out"},
+                           {codes, d, d, "codes"},
+                           {scales, n_group * 4, n_group * 4, "scales"}};
+  for (int i = 0; i < 4; ++i) {
+    if (!outs[i].p) continue;
+    for (const RowSpan& r : in) {
+      const bool in_place = i < 2 && &r != &in[2] && r.p == outs[i].p && (T == 1 || r.step == outs[i].step);
+      if (r.p && !in_place && !rows_disjoint(r, outs[i], T))
+        return fail(GMLA_ERR_INVALID_ARG, "%s overlaps %s without being the same rows", outs[i].name, r.name);
+    }
+    for (int j = i + 1; j < 4; ++j)
+      if (outs[j].p && !rows_disjoint(outs[i], outs[j], T))
+        return fail(GMLA_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, outs[j].name);
   }
   NormArgs a{};
   a.x = x;

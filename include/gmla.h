@@ -321,7 +321,9 @@ GMLA_API gmla_status gmla_plan_batch(const int32_t* cached_lens, const int32_t* 
  *   x            [T, d] (d <= 32768), rows x_stride elements apart, likewise the others
  *   residual     or NULL (s = x);  weight [d] or NULL (all ones)
  *   residual_out gets s, or NULL; may be `residual` or `x` itself
- *   out          gets y, or NULL; may be `x` itself
+ *   out          gets y, or NULL; may be `residual` or `x` itself
+ *   (an output that overlaps an input or another output in any other way is refused; rows
+ *   side by side in one matrix do not overlap)
  *   codes        [T, d] E4M3 codes of y / scale (round to nearest even), with
  *   scales       [T, ceil(d / group)] fp32: max |y| over the group / 448, 1 for a group of
  *                zeros; group 32, 64, 128 or 256. Both NULL with group = 0: no 8-bit output
