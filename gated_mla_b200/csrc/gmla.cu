@@ -1250,24 +1250,25 @@ gmla_status gmla_add_rms_norm(int32_t dtype, const void* x, int64_t x_stride, co
   if ((group != 0) != (codes != nullptr) || (group != 0) != (scales != nullptr))
     return fail(GMLA_ERR_INVALID_ARG, "codes and scales go with a group > 0");
   if (!out && !residual_out && !codes) return fail(GMLA_ERR_INVALID_ARG, "no output is given");
-  GMLA_TRY(check_ptr(x, "x"));
-  GMLA_TRY(check_ptr(residual, "residual", false));
-  GMLA_TRY(check_ptr(weight, "weight", false));
-  GMLA_TRY(check_ptr(residual_out, "residual_out", false));
-  GMLA_TRY(check_ptr(out, "out", false));
-  GMLA_TRY(check_ptr(codes, "codes", false));
-  GMLA_TRY(check_ptr(scales, "scales", false));
-  const struct { const void* p; int64_t s; } rows[4] = {
-      {x, x_stride}, {residual, residual_stride}, {residual_out, residual_out_stride}, {out, out_stride}};
-  bool vec = d % 8 == 0;
+  const int64_t es = dtype == GMLA_FP32 ? 4 : 2, n_group = group ? (d + group - 1) / group : 0;
+  if (!x) return fail(GMLA_ERR_INVALID_ARG, "x is NULL");
+  auto off = [](const void* p, int64_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; };
+  const struct { const void* p; int64_t s; const char* name; } rows[4] = {{x, x_stride, "x"},
+                                                                         {residual, residual_stride, "residual"},
+                                                                         {residual_out, residual_out_stride, "residual_out"},
+                                                                         {out, out_stride, "out"}};
+  // 16-byte accesses (8 bytes of codes) where d, every stride and every address allow them
+  bool vec = d % 8 == 0 && !off(weight, 16) && !off(codes, 8);
   for (const auto& r : rows) {
     if (!r.p) continue;
+    if (off(r.p, es)) return fail(GMLA_ERR_INVALID_ARG, "%s is not aligned to its elements", r.name);
     if (r.s < d && T > 1) return fail(GMLA_ERR_INVALID_ARG, "a row stride is smaller than d");
-    vec = vec && (T == 1 || r.s % (dtype == GMLA_FP32 ? 4 : 8) == 0);
+    vec = vec && !off(r.p, 16) && (T == 1 || r.s * es % 16 == 0);
   }
+  if (off(weight, es)) return fail(GMLA_ERR_INVALID_ARG, "weight is not aligned to its elements");
+  if (off(scales, 4)) return fail(GMLA_ERR_INVALID_ARG, "scales is not 4-byte aligned");
   // A thread reads its elements of x and residual before it stores them, so rows may be written in place; rows that
   // overlap in any other way would be read by one thread after another has written them.
-  const int64_t es = dtype == GMLA_FP32 ? 4 : 2, n_group = group ? (d + group - 1) / group : 0;
   const RowSpan in[3] = {{x, d * es, x_stride * es, "x"},
                          {residual, d * es, residual_stride * es, "residual"},
                          {weight, d * es, 0, "weight"}};

@@ -216,7 +216,7 @@ struct NormArgs {
   float* scales;             // [T, ceil(d / group)]
   int64_t x_stride, residual_stride, residual_out_stride, out_stride;
   int32_t T, d, group;       // group 0: no codes
-  int32_t vec;               // 16-byte accesses: d and every stride allow them
+  int32_t vec;               // 16-byte accesses: d, every stride and every address allow them
   int32_t warps;             // warps a row (set by the launch)
   float eps;
 };

@@ -86,7 +86,7 @@ constexpr int norm_regs(int vpt, bool f32, bool grp) {
 
 // One row per `warps` warps; VPT vectors of 8 elements a thread (vector i of lane t
 // covers elements 8 (i * 32 * warps + t) ..). blockDim = warps * 32 * rows a block.
-// VEC: d and the row strides allow 16-byte accesses, and every vector is whole.
+// VEC: d, the row strides and the addresses allow 16-byte accesses, and every vector is whole.
 template <typename T, int VPT, bool VEC, bool GRP>
 __global__ void __maxnreg__(norm_regs(VPT, sizeof(T) == 4, GRP)) add_rms_norm_kernel(NormArgs a) {
   __shared__ float s_sum[32];

@@ -44,8 +44,9 @@
  *   - The bf16 path runs on tcgen05 tensor cores with fp32 accumulation; the
  *     fp32 path runs on CUDA cores in fp32. There is no CPU fallback: a shape
  *     the kernels do not cover returns GMLA_ERR_UNSUPPORTED.
- *   - All base pointers must be 16-byte aligned. Block tables, and what gmla_plan_batch says
- *     of its own arguments, may start at any element: a batch may be a slice of a larger one.
+ *   - All base pointers must be 16-byte aligned. Block tables, and what gmla_plan_batch and
+ *     gmla_add_rms_norm say of their own arguments, may start at any element: a batch may be a
+ *     slice of a larger one.
  */
 #ifndef GMLA_H_
 #define GMLA_H_
@@ -318,7 +319,8 @@ GMLA_API gmla_status gmla_plan_batch(const int32_t* cached_lens, const int32_t* 
  *   s = x + residual;  y = s / sqrt(mean(s^2) + eps) * weight
  *   dtype        of x, residual, weight, residual_out, out (gmla_dtype); the
  *                arithmetic is fp32, s and y are rounded once, when stored
- *   x            [T, d] (d <= 32768), rows x_stride elements apart, likewise the others
+ *   x            [T, d] (d <= 32768), rows x_stride elements apart, likewise the others; rows
+ *                and weight may start at any element (16-byte boundaries are faster)
  *   residual     or NULL (s = x);  weight [d] or NULL (all ones)
  *   residual_out gets s, or NULL; may be `residual` or `x` itself
  *   out          gets y, or NULL; may be `residual` or `x` itself

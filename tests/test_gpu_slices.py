@@ -43,3 +43,31 @@ def test_the_last_sequences_of_a_table_of_odd_width(width, first):
         model.sync_status()
         bf16.sync_status()
     assert outs[0][0].any() and all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,first,group", [(129, 1, 0), (129, 3, 32), (512, 2, 128), (777, 5, 0), (1000, 1, 64), (7, 1, 0)])
+def test_norm_of_rows_off_a_boundary(dt, d, first, group):
+    """x[first:] of odd rows, columns from the first on, a weight that is a slice: as on copies of them."""
+    import gated_mla_b200 as gmla
+    from test_gpu_add_rms_norm import _check, _inputs
+    wide, weight, rw = _inputs(40, d + first, dt)
+    w = weight[first:]
+    for x, r in ((wide[first:, :d].contiguous().flatten(), rw[first:, :d].contiguous().flatten()),):
+        flat, rflat = torch.cat([x.new_zeros(first), x]), torch.cat([r.new_zeros(first), r])
+        x1, r1 = flat[first:].view(-1, d), rflat[first:].view(-1, d)
+        got = gmla.add_rms_norm(x1, w, r1, fp8_group=group)
+        _check(got, x1, w, r1, group)
+    x2, r2 = wide[:, first:], rw[:, first:]
+    x0, r0, edge = x2.clone(), r2.clone(), wide[:, :first].clone()
+    got = gmla.add_rms_norm(x2, w, r2, fp8_group=group, out=x2, residual_out=r2)
+    _check(got, x0, w, r0, group)
+    assert torch.equal(wide[:, :first], edge)
+
+
+def test_norm_of_one_row_of_an_odd_matrix():
+    import gated_mla_b200 as gmla
+    from test_gpu_add_rms_norm import _check, _inputs
+    x, w, r = _inputs(9, 515, torch.bfloat16)
+    _check(gmla.add_rms_norm(x[7:8], w, r[3:4]), x[7:8], w, r[3:4], 0)
+    _check(gmla.add_rms_norm(x[1:], w, r[:-1]), x[1:], w, r[:-1], 0)
