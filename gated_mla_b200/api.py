@@ -411,12 +411,12 @@ class GatedMLA:
             c = self._status_cfg(q.device)
             with self._scratch.lock:
                 ws = self._scratch.get("decode", nb, q.device, stream)
-                L.check(L.gmla_decode(c, self.w, _p(q), _p(gate_logits), cache.struct(), _p(seq_lens), B,
-                                      _p(o_out), ws.data_ptr(), ws.numel(), stream), "gmla_decode")
+                L.check(L.gmla_decode(c, self.w, _p(q), _p(gate_logits), self.cache_arg(cache, q.device), _p(seq_lens),
+                                      B, _p(o_out), ws.data_ptr(), ws.numel(), stream), "gmla_decode")
             return o_out
         if ws is None:
             ws = self.workspace("decode", nb, q.device)
-        L.check(L.gmla_decode(c, self.w, _p(q), _p(gate_logits), cache.struct(), _p(seq_lens), B,
+        L.check(L.gmla_decode(c, self.w, _p(q), _p(gate_logits), self.cache_arg(cache, q.device), _p(seq_lens), B,
                               _p(o_out), ws.data_ptr(), ws.numel(), self._stream()), "gmla_decode")
         return o_out
 
@@ -471,6 +471,10 @@ class GatedMLA:
         if cache.data.device != device or cache.data.element_size() != 1 or cache.data.shape[-1] != self.row:
             raise ValueError(f"a block-scaled cache holds 1-byte codes in rows of {self.row} on {device}")
         return cache.struct()
+
+    def cache_arg(self, cache: LatentCache, device) -> L.gmla_cache:
+        """The cache argument of a decode (without scales a block-scaled layer's is left to the library to refuse)."""
+        return self._cache_struct(cache, device) if self.block_scaled and cache.scales is not None else cache.struct()
 
     def _project_and_append(self, x, cache, q_out, gate_logits, cu_seqlens, seq_lens):
         if cu_seqlens is None or seq_lens is None:

@@ -58,7 +58,7 @@ def decode_partial(model: GatedMLA, q, gate_logits, cache: LatentCache, seq_star
     if out is None:
         out = torch.empty(B, c.n_heads, partial_width(model), dtype=torch.float32, device=q.device)
     ws = model.workspace("decode", L.gmla_decode_workspace_size(c, B), q.device)
-    L.check(L.gmla_decode_partial(c, model.w, _p(q), _p(gate_logits), cache.struct(), _p(seq_starts),
+    L.check(L.gmla_decode_partial(c, model.w, _p(q), _p(gate_logits), model.cache_arg(cache, q.device), _p(seq_starts),
                                   _p(seq_ends), B, _p(out), ws.data_ptr(), ws.numel(), model._stream()),
             "gmla_decode_partial")
     return out
