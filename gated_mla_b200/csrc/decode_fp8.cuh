@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(128) decode_absorb_tc8_kernel(const __grid_con
 struct Dec8Smem {
   uint64_t full[16], empty[16];   // per ring box
   uint64_t s_full[2], p_full[2], pv_done[2];   // of even and odd tiles where two tiles are in work (kPipe), else the first
-  uint64_t q_full, q_empty, drain2, o_done, o_free, drain, never;
+  uint64_t q_full, q_empty, o_done, o_free, drain, never;
   uint32_t tmem;
   int abort;
   int vote[3];
@@ -455,10 +455,9 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
       mbar_init(&sm->p_full[i], 128 * C::kSG);
       mbar_init(&sm->pv_done[i], 1);
     }
-    mbar_init(&sm->drain2, 1);
     mbar_init(&sm->o_done, 1);
     mbar_init(&sm->o_free, 128 * C::kSG);
-    mbar_init(&sm->drain, 1);
+    mbar_init(&sm->drain, C::kPipe ? 2 : 1);
     mbar_init(&sm->never, 1);
     sm->abort = 0;
     sm->vote[0] = sm->vote[1] = sm->vote[2] = 0;
@@ -477,6 +476,7 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
   const int seg_hi = (seg_lo < a.cta_first_seg[g + 1]) ? a.cta_first_seg[g + 1] : seg_lo;
   const uint32_t tmem = sm->tmem;
   const uint32_t tO = tmem + 2 * N2;   // O^T chunk j (latent dims 128 j ..) at columns tO + j NP
+  uint32_t loaded = 0, loaded_q = 0;   // ring boxes and query tiles requested (producer)
 
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
@@ -538,12 +538,8 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
         }
       }
     }
-    if (lane == 0 && *abort_flag) {   // let issued copies land before the block exits
-      const uint32_t n = (nbox + BP - 1) / BP;
-      for (uint32_t c = n > static_cast<uint32_t>(NB) ? n - NB : 0; c < n; ++c)
-        mbar_drain(&sm->full[c % NB], (c / NB) & 1);
-      if (nq) mbar_drain(&sm->q_full, (nq - 1) & 1);
-    }
+    loaded = nbox;
+    loaded_q = nq;
   } else if (warp == 1 || (C::kPipe && warp == C::kThreads / 32 - 1)) {
     // ------------------------------ MMA issuers ------------------------------
     if constexpr (BLK) {   // whole warps, converged (see umma_f8_warp)
@@ -617,11 +613,6 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
           if (sums) umma_commit_warp(&sm->o_done);
           ++nseg;
         }
-        if (!ok) {
-          uint64_t* drain = sums ? &sm->drain2 : &sm->drain;
-          umma_commit_warp(drain);
-          mbar_drain(drain, 0);
-        }
       } else {
         int early = 0;
         if (a.test_stall && g == 0 && hg == 0) ok = wait(&sm->never, 0);
@@ -655,10 +646,6 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
           if (!ok) break;
           umma_commit_warp(&sm->o_done);
           ++nseg;
-        }
-        if (!ok) {
-          umma_commit_warp(&sm->drain);
-          mbar_drain(&sm->drain, 0);
         }
       }
     } else if (lane == 0) {
@@ -721,10 +708,6 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
         if (!ok) break;
         umma_commit(&sm->o_done);
         ++nseg;
-      }
-      if (!ok) {
-        umma_commit(&sm->drain);
-        mbar_drain(&sm->drain, 0);
       }
     }
   } else {
@@ -999,6 +982,24 @@ __global__ void __launch_bounds__(64 + 128 * (HG >= 32 ? 2 : 1) + (BLK && HG == 
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  // A wait gave up: copies land and products end before their memory goes. Here every role has left its loop and the
+  // flag is settled; a role that ran to its end while another gave up has nobody else to wait for what it issued.
+  if (*abort_flag) {
+    if (warp == 0 && lane == 0) {
+      const uint32_t n = (loaded + BP - 1) / BP;
+      for (uint32_t c = n > static_cast<uint32_t>(NB) ? n - NB : 0; c < n; ++c)
+        mbar_drain(&sm->full[c % NB], (c / NB) & 1);
+      if (loaded_q) mbar_drain(&sm->q_full, (loaded_q - 1) & 1);
+    }
+    if (warp == 1 || (C::kPipe && warp == C::kThreads / 32 - 1)) {
+      if (BLK)
+        umma_commit_warp(&sm->drain);
+      else if (lane == 0)
+        umma_commit(&sm->drain);
+      mbar_drain(&sm->drain, 0);
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
