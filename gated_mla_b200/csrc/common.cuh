@@ -21,10 +21,12 @@ struct CacheView {
   int32_t row;          // d_c + d_R
 };
 
-// Most rows a sequence may have (a wide table times a large page passes 32 bits: lengths do not).
+// Most rows a sequence may have: a wide table times a large page passes 32 bits, lengths do not. The last 255 numbers
+// are left out, so that a length rounds up to whole tiles.
 __host__ __device__ inline int cache_limit(const CacheView& c) {
+  constexpr int kMost = 0x7fffff00;
   const int64_t rows = c.paged ? static_cast<int64_t>(c.max_pages_per_seq) * c.page_size : c.capacity;
-  return rows < 0x7fffffff ? static_cast<int>(rows) : 0x7fffffff;
+  return rows < kMost ? static_cast<int>(rows) : kMost;
 }
 
 // Global row index of token `pos` of sequence `b`, or -1 when out of range.
