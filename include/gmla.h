@@ -329,7 +329,10 @@ GMLA_API gmla_status gmla_plan_batch(const int32_t* cached_lens, const int32_t* 
  *   codes        [T, d] E4M3 codes of y / scale (round to nearest even), with
  *   scales       [T, ceil(d / group)] fp32: max |y| over the group / 448, 1 for a group of
  *                zeros; group 32, 64, 128 or 256. Both NULL with group = 0: no 8-bit output
- * A row with a NaN or an infinity gives NaN in y and undefined codes.
+ * A NaN makes its row of y NaN; an infinity gives NaN in its place and 0 beside it, as the
+ * formula does. Both leave the row's codes undefined. The squares are summed in fp32: a row
+ * whose sum passes its range (elements beyond about 1e19) gives 0, one whose squares all
+ * underflow (below about 1e-23) under eps = 0 an infinity.
  * ------------------------------------------------------------------------- */
 GMLA_API gmla_status gmla_add_rms_norm(int32_t dtype, const void* x, int64_t x_stride,
                                        const void* residual, int64_t residual_stride,
