@@ -401,6 +401,8 @@ class GatedMLA:
         return q_out, gate_logits
 
     def decode(self, q, gate_logits, cache: LatentCache, seq_lens, o_out=None, ws=None):
+        """One query for each sequence: row b of ``q`` attends to the first seq_lens[b] cached rows of sequence b.
+        Where plan_batch packs tokens of a batch with idle sequences in between, gather them by sequence first."""
         B = q.shape[0]
         c = self.cfg
         if o_out is None:
@@ -539,7 +541,9 @@ class GatedMLA:
     def decode_step(self, x, cache: LatentCache, seq_lens, positions, seq_ids, *, cu_seqlens=None,
                     w4: Optional[W4Weight] = None):
         """One decode step: project (writing each new latent row), attend, gate, W_o (in 4
-        bits when ``w4`` is given). A block-scaled cache needs the step's ``cu_seqlens``."""
+        bits when ``w4`` is given). Row b of ``x`` is sequence b's token: sequences that get none in this
+        step come last (``decode`` takes row b of its queries as sequence b's). A block-scaled cache
+        needs the step's ``cu_seqlens``."""
         if self.block_scaled:
             q, g = self.latent_project(x, positions, seq_ids, cache, cu_seqlens=cu_seqlens, seq_lens=seq_lens)
         else:

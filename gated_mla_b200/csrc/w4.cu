@@ -138,7 +138,9 @@ __device__ __forceinline__ void w4_gated8(const W4PrepArgs& a, int t, int k, flo
 constexpr uint32_t kW4Large = 0x7180;
 
 // ---------------------------------------------------------------------------
-// a = gate ⊙ o in bf16, in fragment order, and -136 times its sum over each group.
+// a = gate ⊙ o in bf16, in fragment order, and -136 times its sum over each group. (bf16: the
+// codes' operand 128 + v is, and both operands of the instruction have one type. So the gated product is rounded
+// to 2^-8, as gate_out's is, and the result's error is 0.0023 instead of 0.0017; without a gate nothing is rounded.)
 // out: for each token tile of 8 nt and each chunk of 256 k, [8 steps][nt][g * 4 + c][8 bf16]: token 8 n + g of the
 // tile, k = 32 step + 8 c + (0 4 1 5 2 6 3 7), then the sums [256 / group][8 nt] fp32 in 256 nt bytes.
 // Tokens and k behind the end are zeros. A thread makes one run of 8 k; the runs of a group are
