@@ -8,6 +8,7 @@ computation happens inside libgmla.so on the current CUDA stream.
 """
 from __future__ import annotations
 
+import ctypes
 import dataclasses
 import math
 import threading
@@ -368,6 +369,8 @@ class GatedMLA:
             if staging:
                 cfg.cache_dtype = L.GMLA_CACHE_SAME
             self._cfgs[(device.index, staging)] = cfg
+        elif not staging:      # what the layer's configuration says by now
+            ctypes.memmove(ctypes.addressof(cfg), ctypes.addressof(self.cfg), L.gmla_config.status.offset)
         return cfg
 
     @staticmethod
