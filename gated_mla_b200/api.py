@@ -8,7 +8,6 @@ computation happens inside libgmla.so on the current CUDA stream.
 """
 from __future__ import annotations
 
-import ctypes
 import dataclasses
 import math
 import threading
@@ -341,7 +340,8 @@ class GatedMLA:
         self._ws = {}
         self._scratch = _shared_scratch()     # workspaces of the calls that report into the layer's word
         self._status = _Scratch()             # that word
-        self._cfgs = {}
+        self._status_on = -1                  # the device whose word the configuration names
+        self._staging_cfg = None
 
     # -- sizes
     @property
@@ -362,16 +362,16 @@ class GatedMLA:
 
     def _status_cfg(self, device: torch.device, staging: bool = False) -> L.gmla_config:
         """The configuration with the layer's status word on the device; `staging`: the same layer over a bf16 cache."""
-        cfg = self._cfgs.get((device.index, staging))
-        if cfg is None:
+        if self._status_on != device.index:
+            self.cfg.status = self._status.word("layer", device).data_ptr()
+            self._status_on, self._staging_cfg = device.index, None
+        if not staging:
+            return self.cfg
+        if self._staging_cfg is None:
             cfg = L.gmla_config.from_buffer_copy(self.cfg)
-            cfg.status = self._status.word("layer", device).data_ptr()
-            if staging:
-                cfg.cache_dtype = L.GMLA_CACHE_SAME
-            self._cfgs[(device.index, staging)] = cfg
-        elif not staging:      # what the layer's configuration says by now
-            ctypes.memmove(ctypes.addressof(cfg), ctypes.addressof(self.cfg), L.gmla_config.status.offset)
-        return cfg
+            cfg.cache_dtype = L.GMLA_CACHE_SAME
+            self._staging_cfg = cfg
+        return self._staging_cfg
 
     @staticmethod
     def _stream() -> int:
